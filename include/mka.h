@@ -237,6 +237,54 @@ MKA_API int mka_prefill_backward(const mka_config* cfg, const void* packed, cons
 MKA_API int mka_decode_step(const mka_config* cfg, const void* packed, void* state, size_t state_bytes,
                     int32_t max_positions, const void* x_new, void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ window attention with sinks
+ * Causal GQA attention bounded in memory: position t of a sequence sees position j iff
+ *   j <= t  and  (window == 0  or  j > t - window  or  j < sinks),
+ * its last `window` positions, itself among them, and the first `sinks` of the sequence (the layer's
+ * local memory, notes §1, as an attention of its own).  out = softmax(scale * q k^T over the seen j) v,
+ * online max-shift (notes §4); sums and softmax statistics are float32, the probabilities enter the
+ * product with v rounded to bf16.  bf16 tensors, d_head 64 or 128; float32 is MKA_ERR_UNSUPPORTED.
+ *   - lens (nullable) [batch] int32: rows in use per sequence, clamped to [0, seq]; NULL: all.  Rows at
+ *     or past lens[b] (a padded batch) are not read into any result, whatever they hold, and the same
+ *     rows of every output are left as they were.
+ *   - A NaN or infinity in a row in use can reach every row in use whose 128-row tile shares a visible
+ *     pair with that row's 128-row tile, hidden pairs included.
+ *   - strides (nullable): see mka_attn_strides; NULL: dense tensors.
+ *   - No tensor may overlap an output. */
+typedef struct mka_attn_config {
+  int32_t batch;      /* B */
+  int32_t seq;        /* S */
+  int32_t n_q_heads;  /* Hq, a multiple of n_kv_heads; query head h reads KV head h / (Hq / Hkv) */
+  int32_t n_kv_heads; /* Hkv */
+  int32_t d_head;     /* 64 or 128 */
+  int32_t dtype;      /* MKA_BF16 */
+  int32_t window;     /* positions seen, the own one among them; 0: every earlier one */
+  int32_t sinks;      /* first positions that stay visible behind the window */
+  float attn_scale;   /* <= 0 selects 1/sqrt(d_head) */
+} mka_attn_config;
+
+/* Row strides in elements of q, k, v, out and dout [B, S, heads * d_head], multiples of 8 and at least
+ * heads * d_head (0: exactly that): row t of sequence b starts at (b * S + t) * stride, so the tensors
+ * may be column ranges of one packed projection. */
+typedef struct mka_attn_strides {
+  int32_t q, k, v, out, dout;
+} mka_attn_strides;
+
+/* q [B, S, Hq*dh], k, v [B, S, Hkv*dh] -> out [B, S, Hq*dh].  lse (nullable) [B, Hq, S rounded up to a
+ * multiple of 128] float32 receives each row's softmax normaliser in log2 units, for the backward. */
+MKA_API int mka_window_attention(const mka_attn_config* cfg, const mka_attn_strides* strides, const void* q,
+                                 const void* k, const void* v, const int32_t* lens, void* out, float* lse, void* stream);
+/* Bytes of scratch that mka_window_attention_backward needs for cfg (0 on a bad cfg). */
+MKA_API size_t mka_window_attention_backward_workspace_size(const mka_attn_config* cfg);
+/* Gradients of L = sum(dout * out) over the rows in use, from out and lse of mka_window_attention on the
+ * same q, k, v, lens: dq [B, S, Hq*dh], dk, dv [B, S, Hkv*dh] bf16, dense (dk and dv summed over the
+ * query heads of a KV head in float32, in a fixed order).  ws: 16-byte aligned scratch, used by one call
+ * at a time. */
+MKA_API int mka_window_attention_backward(const mka_attn_config* cfg, const mka_attn_strides* strides, const void* q,
+                                          const void* k, const void* v, const void* out, const float* lse,
+                                          const void* dout, const int32_t* lens, void* dq, void* dk, void* dv, void* ws,
+                                          size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ without caller scratch */
 
 /* Bytes of the library's built-in scratch used by mka_session_ema_noalloc. */

@@ -42,7 +42,8 @@ EXPORTED = [
     "mka_state_init", "mka_router", "mka_session_ema", "mka_longterm_recall", "mka_prefill_forward",
     "mka_decode_step", "mka_status", "mka_last_error", "mka_version", "mka_profile_enable", "mka_profile_read",
     "mka_session_ema_noalloc", "mka_selftest_wait_timeout", "mka_train_workspace_size", "mka_prefill_forward_train",
-    "mka_prefill_backward", "mka_set_wait_limit",
+    "mka_prefill_backward", "mka_set_wait_limit", "mka_window_attention",
+    "mka_window_attention_backward_workspace_size", "mka_window_attention_backward",
 ]
 
 
@@ -61,6 +62,16 @@ class mka_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w_q", "w_k", "w_v", "w_r1", "w_r2", "hash_proj")]
 
 
+class mka_attn_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "seq", "n_q_heads", "n_kv_heads", "d_head", "dtype", "window",
+                                              "sinks")] + [("attn_scale", ctypes.c_float)]
+
+
+class mka_attn_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q", "k", "v", "out", "dout")]
+
+
+_acp, _asp = ctypes.POINTER(mka_attn_config), ctypes.POINTER(mka_attn_strides)
 _vp, _sz, _i32, _cfgp = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(mka_config)
 _SIGS = {
     "mka_packed_weights_size": (_sz, [_cfgp]),
@@ -89,6 +100,9 @@ _SIGS = {
     "mka_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int, _vp, _vp]),
     "mka_set_wait_limit": (ctypes.c_int, [ctypes.c_ulonglong, ctypes.c_int]),
     "mka_profile_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_float), ctypes.c_int]),
+    "mka_window_attention": (ctypes.c_int, [_acp, _asp] + [_vp] * 7),
+    "mka_window_attention_backward_workspace_size": (_sz, [_acp]),
+    "mka_window_attention_backward": (ctypes.c_int, [_acp, _asp] + [_vp] * 11 + [_sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -228,6 +242,102 @@ def mka_decode_step(c: mka_config, packed, state, max_positions: int, x_new, out
     _check(_lib.mka_decode_step(ctypes.byref(c), _ptr(packed), _ptr(state), state.numel() * state.element_size(),
                                 max_positions, _ptr(x_new), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                 _stream(stream)), "mka_decode_step")
+
+
+# ------------------------------------------------------------------ bounded-memory attention
+def _dtype(t: torch.Tensor, want: torch.dtype, name: str) -> None:
+    if t.dtype != want:
+        raise ValueError(f"{name} must be {want}, not {t.dtype}")
+
+
+def _call_stream(tensors, stream):
+    """The stream pointer of a call on `tensors`: they must live on the current device, and a stream
+    other than the current one is recorded on them."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"every tensor of the call must live on the current CUDA device ({dev})")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _dense(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, *shape: int):
+    """Pointer of a contiguous tensor of that type and number of elements (None passes)."""
+    if t is None:
+        return None
+    _dtype(t, dtype, name)
+    n = 1
+    for s in shape:
+        n *= s
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {shape} elements, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, S: int, heads: int, dh: int) -> int:
+    """Row stride of t [B, S, heads, dh] or [B, S, heads * dh] (see mka_attn_strides)."""
+    _dtype(t, dtype, name)
+    width = heads * dh
+    if t.shape != (B, S, heads, dh) and t.shape != (B, S, width):
+        raise ValueError(f"{name} must be [{B}, {S}, {heads}, {dh}] or [{B}, {S}, {width}], not {tuple(t.shape)}")
+    if t.is_contiguous():
+        return width
+    st = t.stride()
+    ld = st[1] if S > 1 else (st[0] if B > 1 else width)
+    if st[-1] != 1 or (len(st) == 4 and heads > 1 and st[2] != dh) or (B > 1 and st[0] != S * ld):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced over the whole batch, strides {st}")
+    return ld
+
+
+def make_attn_config(batch: int, seq: int, n_q_heads: int, n_kv_heads: int, d_head: int, window: int = 0, sinks: int = 0,
+                     attn_scale: Optional[float] = None) -> mka_attn_config:
+    """Shape of a window attention call: window 0 sees every earlier position."""
+    return mka_attn_config(batch=batch, seq=seq, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, d_head=d_head,
+                           dtype=MKA_BF16, window=window, sinks=sinks, attn_scale=attn_scale or 0.0)
+
+
+def attention_lse(c: mka_attn_config, device="cuda") -> torch.Tensor:
+    """Buffer of the softmax normalisers that mka_window_attention leaves for its backward."""
+    return torch.empty(c.batch, c.n_q_heads, (c.seq + 127) // 128 * 128, dtype=torch.float32, device=device)
+
+
+def _lse_ptr(c: mka_attn_config, lse):
+    return _dense(lse, "lse", torch.float32, c.batch, c.n_q_heads, (c.seq + 127) // 128 * 128)
+
+
+def mka_window_attention(c: mka_attn_config, q, k, v, lens, out, lse=None, stream=None) -> None:
+    """q, out [B, S, Hq, dh] (or flat heads), k, v [B, S, Hkv, dh] bf16, row strides allowed; lens [B] int32
+    or None; lse from attention_lse() or None."""
+    bf, B, S, H, G, d = torch.bfloat16, c.batch, c.seq, c.n_q_heads, c.n_kv_heads, c.d_head
+    s = _call_stream((q, k, v, lens, out, lse), stream)
+    st = mka_attn_strides(_row_stride(q, "q", bf, B, S, H, d), _row_stride(k, "k", bf, B, S, G, d),
+                          _row_stride(v, "v", bf, B, S, G, d), _row_stride(out, "out", bf, B, S, H, d), 0)
+    _check(_lib.mka_window_attention(c, st, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                     _dense(lens, "lens", torch.int32, B), out.data_ptr(), _lse_ptr(c, lse), s),
+           "mka_window_attention")
+
+
+def mka_window_attention_backward_workspace_size(c: mka_attn_config) -> int:
+    return _lib.mka_window_attention_backward_workspace_size(c)
+
+
+def mka_window_attention_backward(c: mka_attn_config, q, k, v, out, lse, dout, lens, dq, dk, dv, ws, stream=None) -> None:
+    """Gradients of sum(dout * out) after mka_window_attention(c, q, k, v, lens, out, lse): dq, dk, dv bf16, dense."""
+    bf, B, S, H, G, d = torch.bfloat16, c.batch, c.seq, c.n_q_heads, c.n_kv_heads, c.d_head
+    s = _call_stream((q, k, v, out, lse, dout, lens, dq, dk, dv, ws), stream)
+    st = mka_attn_strides(_row_stride(q, "q", bf, B, S, H, d), _row_stride(k, "k", bf, B, S, G, d),
+                          _row_stride(v, "v", bf, B, S, G, d), _row_stride(out, "out", bf, B, S, H, d),
+                          _row_stride(dout, "dout", bf, B, S, H, d))
+    _check(_lib.mka_window_attention_backward(
+        c, st, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _lse_ptr(c, lse), dout.data_ptr(),
+        _dense(lens, "lens", torch.int32, B), _dense(dq, "dq", bf, B, S, H * d), _dense(dk, "dk", bf, B, S, G * d),
+        _dense(dv, "dv", bf, B, S, G * d), ws.data_ptr(), ws.numel() * ws.element_size(), s),
+        "mka_window_attention_backward")
 
 
 def mka_status() -> int:

@@ -317,6 +317,8 @@ int mka::set_last_error(int code, const char* msg) {
   return code;
 }
 
+int* mka::device_status() { return status_ptr(); }
+
 extern "C" {
 
 const char* mka_version(void) { return "fastmka-b200 0.1 (sm_100a)"; }

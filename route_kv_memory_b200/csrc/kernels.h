@@ -9,6 +9,8 @@ namespace mka {
 
 // Records `msg` as the calling thread's mka_last_error() text; returns `code`.
 int set_last_error(int code, const char* msg);
+// Status block of the current device (see common.cuh); nullptr without a device.
+int* device_status();
 
 // One column range of a GEMM output and where it is stored.
 struct OutSeg {
@@ -138,6 +140,13 @@ struct AttnArgs {
   // scores taken as scale * log2(e) * q.k, at lse[(b * Hq + h) * lse_ld + t] (for the backward)
   float* lse = nullptr; int lse_ld = 0;
   int chunk = 1;  // causal mode: (sequence, KV group) streams per chunk of the work order (set by attention_prefill_tc)
+  // Window with sinks (bf16, tcgen05 only), when windowed: position t sees j <= t with j > t - window
+  // or j < sinks (window 0: every j <= t) over the first lens[b] rows of sequence b (null: S); rows at
+  // or past lens[b] are neither read into a result nor written.  window <= S, sinks <= S.
+  bool windowed = false;
+  int window = 0, sinks = 0;
+  const int* lens = nullptr;
+  long long v_bstride = 0; int v_ld = 0;  // V's own strides (0: kv_bstride, kv_ld)
   // Block-gathered attention (set g_pairoff to select it; bf16, tcgen05 only).  The rows of a
   // work item are (token, query head) pairs that all attend to the keys of one L3 block j of
   // sequence b: the tokens of block j's list (its own tokens first when g_own, under the causal
@@ -195,8 +204,20 @@ struct AttnBwdArgs {
   float* dkv;  // [B][S][2*Hkv*dh] float32: dK then dV per row, 32-byte aligned
   int B, S, Hq, Hkv, dh;
   float scale;
+  // Window with sinks (window_attention_backward_tc): see AttnArgs; bf16 gradients, dense
+  int window = 0, sinks = 0;
+  const int* lens = nullptr;
+  void *dq16 = nullptr, *dk16 = nullptr, *dv16 = nullptr;
+  float* sink_part = nullptr;  // [B][Hkv][1 + far_chunks][sinks][2 dh] partial dK | dV of the sinks
+  int sink_tiles = 0, far_chunks = 0, far_tiles = 1;  // set by window_attention_backward_tc
 };
 cudaError_t attention_backward_tc(const AttnBwdArgs& a, int* status, cudaStream_t s);
+// Row strides (elements) of the windowed backward's operands; sequences are S rows apart.
+struct AttnBwdStrides { int q, k, v, o, dout; };
+// Scratch of the windowed backward: D, then (at *part) the sinks' partial sums.
+size_t window_attention_backward_scratch(int B, int S, int Hq, int Hkv, int dh, int window, int sinks, size_t* part);
+cudaError_t window_attention_backward_tc(const AttnBwdArgs& a, const AttnBwdStrides& ld, const void* o, float* dsum,
+                                         int* status, cudaStream_t s);
 // dsum[(b * Hq + h) * ld + t] = sum_i dO * O over head h of token t (bf16 inputs).
 cudaError_t attention_dsum(const void* dout, const void* o, int B, int S, int Hq, int dh, int ld, float* dsum,
                            cudaStream_t s);

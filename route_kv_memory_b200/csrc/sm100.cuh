@@ -88,6 +88,10 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
+// Orders this thread's generic shared-memory writes before later async-proxy reads (MMA operands);
+// follow it with a barrier before another thread issues those.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 // 2-D tiled load of the box at (x, y) (x innermost) into shared memory; completes
 // `bytes` of transaction count on `bar`.  x * element size must be a multiple of 16.

@@ -25,6 +25,14 @@
 // with TMA (tile::gather4) into the same swizzled tile layout; each row keeps its own softmax
 // over the block's key tiles (the causal mask only for the block's own tokens) and leaves O / l
 // in bf16 with its log2 normaliser for the merge.
+//
+// MODE 2 (window with sinks): causal attention in which position t sees the last `window` positions
+// and the first `sinks` ones, over lens[b] rows of sequence b.  An item streams only the key tiles
+// that some row of its two query tiles sees: first the tile lo holding tile 0's oldest window key
+// (read by tile 0 alone when tile 1's window starts behind it and it holds no sink), then the sink
+// tiles before lo, then lo + 1 up to the diagonal; the order of keys does not matter to the softmax.
+// Only tiles crossed by the diagonal, the window's edge or the sinks' end are masked.  V rows at or
+// past lens[b] are cleared in shared memory before P V: their P is 0, but 0 * NaN is not.
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
@@ -116,6 +124,37 @@ __device__ __forceinline__ int entry_token(int v, int S, int* slot) {
   return v >= 0 && t < S ? t : -1;
 }
 
+// MODE 2 work item: query tiles 2 pair and 2 pair + 1 of head h of sequence b (len rows in use).
+// Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
+struct WWork {
+  int b, h, pair, len, lo, nsk, n0, n1, s1;
+  __device__ __forceinline__ int key_tile(int j) const { return j == 0 ? lo : (j <= nsk ? j - 1 : lo + j - nsk); }
+};
+__device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, int npairs) {
+  const Work it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
+  WWork r;
+  r.b = it.b;
+  r.h = it.h;
+  r.pair = it.pair;
+  r.len = a.lens ? min(max(a.lens[it.b], 0), a.S) : a.S;
+  r.n0 = r.n1 = r.s1 = r.lo = r.nsk = 0;
+  const int qt = 2 * it.pair;
+  if (qt * BQ >= r.len) return r;
+  const int last = (r.len - 1) / BKV;
+  const int lo0 = a.window ? max(0, qt * BQ - a.window + 1) / BKV : 0;
+  const int lo1 = a.window ? max(0, (qt + 1) * BQ - a.window + 1) / BKV : 0;
+  const int hi1 = min(qt + 1, last);
+  r.lo = lo0;
+  r.nsk = min((a.sinks + BKV - 1) / BKV, lo0);
+  r.n0 = 1 + r.nsk + qt - lo0;
+  r.n1 = 1 + r.nsk + hi1 - lo0;
+  r.s1 = lo1 > lo0 && lo0 * BKV >= a.sinks && hi1 > lo0 ? 1 : 0;
+  return r;
+}
+
+// Bits [0, n) of a 32-bit word, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -123,7 +162,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 
-// MODE 0: causal attention; MODE 1: block-gathered rows (see the top of the file).
+// MODE 0: causal attention; MODE 1: block-gathered rows; MODE 2: window with sinks (see the top of
+// the file).
 template <int DH, int MODE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -153,7 +193,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  constexpr bool GA = MODE == 1;
+  constexpr bool GA = MODE == 1, WN = MODE == 2;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
@@ -306,12 +346,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // L2: a query tile is read by this item only, while the K/V of the chunk's streams are read
       // by every item of the chunk: the Q tiles (and the O rows) must not age the K/V out of L2
       const uint64_t pol_once = policy_evict_first(), pol_kv = policy_evict_last();
-      int kvit = 0;
+      int kvit = 0, done = 0;
       for (int rr = 0; rr * (int)gridDim.x < nwork; ++rr) {
         const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
         if (w < 0) break;
-        const int wi = rr;  // items this CTA has started before this one
-        const Work it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
+        Work it;
+        WWork ww;
+        if constexpr (WN) {
+          ww = window_item(w, a, npairs);
+          if (ww.n1 == 0) continue;  // (every role skips the same items)
+          it = {ww.b, ww.h, ww.pair};
+        } else {
+          it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
+        }
+        const int wi = done++;  // items this CTA has started before this one
         const int g = it.h / G;
         bool qok = true;
         for (int t = 0; t < 2; ++t) {  // each tile as soon as the previous item's last S_t has read it
@@ -325,7 +373,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tma_load_2d_hint(sQ + t * C::Q_BYTES + hb * C::HALF, &tmQ, &q_full[t], it.h * DH + hb * 64, qy, pol_once);
         }
         if (!qok) break;
-        const int nkv = 2 * it.pair + 2;
+        const int nkv = WN ? ww.n1 : 2 * it.pair + 2;
         bool ok = true;
         for (int j = 0; j < nkv; ++j, ++kvit) {
           const int st = kvit & 1;
@@ -335,7 +383,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           mbar_expect_tx(&kv_full[st], C::KV_BYTES);
           uint8_t* kdst = sKV + st * C::KV_BYTES;
-          const int ky = (int)(it.b * kv_rows_per_b) + j * BKV;
+          const int ky = (int)(it.b * kv_rows_per_b) + (WN ? ww.key_tile(j) : j) * BKV;
           for (int hb = 0; hb < NH; ++hb) {
             tma_load_2d_hint(kdst + hb * C::HALF, &tmK, &kv_full[st], g * DH + hb * 64, ky, pol_kv);
             tma_load_2d_hint(kdst + C::K_BYTES + hb * C::HALF, &tmV, &kv_full[st], g * DH + hb * 64, ky, pol_kv);
@@ -347,8 +395,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp runs the role, converged; one elected lane issues)
-    int kvit = 0, pc[2] = {0, 0};
+    int kvit = 0, pc[2] = {0, 0}, done = 0;
     bool ok = true;
+    WWork ww = {};
+    // The K/V tile of step j (key tile kt of the current item) has landed in its stage; MODE 2 clears
+    // the V rows at or past the sequence's end.
+    auto kv_ready = [&](int cur, int kt) {
+      if (!mbar_wait_warp(&kv_full[cur & 1], (cur >> 1) & 1, abort, status)) return false;
+      if constexpr (WN) {
+        const int used = ww.len - kt * BKV;
+        if (used < BKV) {
+          uint8_t* v = sKV + (cur & 1) * C::KV_BYTES + C::K_BYTES;
+          for (int i = used * 8 + lane; i < BKV * 8; i += 32)  // 16-byte pieces: 8 per 64-column row
+            for (int hb = 0; hb < NH; ++hb) *(uint4*)(v + hb * C::HALF + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+          __syncwarp();
+        }
+      }
+      return true;
+    };
     const uint64_t qd0 = sdesc_kmajor_sw128(sQ), qd1 = sdesc_kmajor_sw128(sQ + C::Q_BYTES);
     auto issue_s = [&](int t, int st) {
       const uint64_t kd = sdesc_kmajor_sw128(sKV + st * C::KV_BYTES);
@@ -367,22 +432,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int k4 = 0; k4 < BKV / 32; ++k4) {
         const int kk = hh * (BKV / 32) + k4;
         umma_bf16_ts_w(tbase + O_COL(t), tbase + S_COL(t) + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)), IDESC_O,
-                       (j | kk) != 0);
+                       (WN ? (kk != 0 || j != (t ? ww.s1 : 0)) : (j | kk) != 0));
       }
       if (hh) umma_commit_w(&pv_done[t]);
     };
     int nx0 = 0, nx1 = 0;  // tiles of the next item, looked up while this one runs
-    {
+    if constexpr (!WN) {
       const int w0 = snake_item(0, gridDim.x, blockIdx.x, nwork);
       if (w0 >= 0) item_tiles(w0, nx0, nx1);
     }
     for (int rr = 0; rr * (int)gridDim.x < nwork && ok; ++rr) {
       const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
-      const int wi = rr;  // items this CTA has started before this one
+      if constexpr (WN) {
+        ww = window_item(w, a, npairs);
+        if (ww.n1 == 0) continue;
+        nx0 = ww.n0;
+        nx1 = ww.n1;
+      }
+      const int wi = done++;  // items this CTA has started before this one
       const int n0 = nx0, n1 = nx1;  // n0 <= n1, n1 >= 1
+      const int s1 = WN ? ww.s1 : 0;  // tile 1's first step
       if (!mbar_wait_warp(&q_full[0], wi & 1, abort, status)) break;
-      if (n1 > 0 && !mbar_wait_warp(&kv_full[kvit & 1], (kvit >> 1) & 1, abort, status)) break;
+      if (n1 > 0 && !kv_ready(kvit, WN ? ww.lo : 0)) break;
       tc_fence_after();
       if (n0 > 0) issue_s(0, kvit & 1);
       if (n0 <= 1) umma_commit_w(&q_empty[0]);  // Q_0's last use (or none)
@@ -396,13 +468,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (!mbar_wait_warp(&q_full[1], wi & 1, abort, status)) break;
       tc_fence_after();
-      if (n1 > 0) issue_s(1, kvit & 1);
+      if (n1 > 0 && s1 == 0) issue_s(1, kvit & 1);
       if (n1 <= 1) umma_commit_w(&q_empty[1]);
       if (n1 == 0) {
         if (!mbar_wait_warp(&o_empty[1], (wi & 1) ^ 1, abort, status)) break;
         umma_commit_w(&o_full[1]);
       }
-      {  // the next item's tile counts, looked up while these S MMAs and the softmax run
+      if constexpr (!WN) {  // the next item's tile counts, looked up while these S MMAs and the softmax run
         const int wn = snake_item(rr + 1, gridDim.x, blockIdx.x, nwork);
         if (wn >= 0) item_tiles(wn, nx0, nx1);
       }
@@ -420,25 +492,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ++pc[0];
           if (j + 1 == n0) umma_commit_w(&o_full[0]);
           if (j + 1 < n0) {
-            if (!mbar_wait_warp(&kv_full[nst], ((cur + 1) >> 1) & 1, abort, status)) { ok = false; break; }
+            if (!kv_ready(cur + 1, WN ? ww.key_tile(j + 1) : 0)) { ok = false; break; }
             tc_fence_after();
             next_ready = true;
             issue_s(0, nst);
             if (j + 2 == n0) umma_commit_w(&q_empty[0]);  // Q_0's last use
           }
         }
-        if (!mbar_wait_warp(&p_half[1], pc[1] & 1, abort, status)) { ok = false; break; }
-        if (j == 0 && !mbar_wait_warp(&o_empty[1], (wi & 1) ^ 1, abort, status)) { ok = false; break; }
-        tc_fence_after();
-        issue_pv_half(1, st, j, 0);
-        if (!mbar_wait_warp(&p_full[1], pc[1] & 1, abort, status)) { ok = false; break; }
-        tc_fence_after();
-        issue_pv_half(1, st, j, 1);
-        ++pc[1];
+        if (!WN || j >= s1) {
+          if (!mbar_wait_warp(&p_half[1], pc[1] & 1, abort, status)) { ok = false; break; }
+          if (j == s1 && !mbar_wait_warp(&o_empty[1], (wi & 1) ^ 1, abort, status)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv_half(1, st, j, 0);
+          if (!mbar_wait_warp(&p_full[1], pc[1] & 1, abort, status)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv_half(1, st, j, 1);
+          ++pc[1];
+        }
         umma_commit_w(&kv_empty[st]);
         if (j + 1 < n1) {
           if (!next_ready) {
-            if (!mbar_wait_warp(&kv_full[nst], ((cur + 1) >> 1) & 1, abort, status)) { ok = false; break; }
+            if (!kv_ready(cur + 1, WN ? ww.key_tile(j + 1) : 0)) { ok = false; break; }
             tc_fence_after();
           }
           issue_s(1, nst);
@@ -468,11 +542,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // causal output rows start on 32-byte boundaries: one 32-byte store per 16 columns
     const bool o32 = !GA && ((uintptr_t)a.o & 31) == 0 && a.o_ld % 16 == 0 && a.o_bstride % 16 == 0;
     const uint64_t pol_out = policy_evict_first();  // output rows: written once, not read here
-    int sit = 0;
+    int sit = 0, done = 0;
     for (int rr = 0; rr * (int)gridDim.x < nwork; ++rr) {
       const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
-      const int wi = rr;
+      WWork ww;
+      int j0 = 0;  // first step of this tile
+      if constexpr (WN) {
+        ww = window_item(w, a, npairs);
+        if (ww.n1 == 0) continue;
+      }
+      const int wi = done++;
       // This row: causal, position `row` of query head h of sequence b; MODE 1, the token of
       // entry e of the item's list (-1 for a padding row), query head h of KV group g.
       int b, h, row, nkv, slot = 0, key0 = 0;
@@ -488,6 +568,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         key0 = it.j * a.blk;  // keys of the block's tiles start here
         row_lim = row >= 0 && row / a.blk == it.j ? row : kNoMask;  // the block's own tokens only
         masked = __any_sync(0xffffffffu, row_lim != kNoMask);
+      } else if constexpr (WN) {
+        b = ww.b;
+        h = ww.h;
+        row = (2 * ww.pair + t) * BQ + r;
+        j0 = t ? ww.s1 : 0;
+        nkv = t ? ww.n1 : ww.n0;
+        row_lim = row;
+        masked = false;
       } else {
         const Work it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
         const int qt = 2 * it.pair + t;
@@ -500,12 +588,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < nkv; ++j, ++sit) {
+      for (int j = j0; j < nkv; ++j, ++sit) {
         if (!mbar_wait_warp(&s_full[t], sit & 1, abort, status)) { ok = false; break; }
         tc_fence_after();
-        const bool diag = GA ? masked : (j == nkv - 1);
+        bool diag = GA ? masked : (j == nkv - 1);
         // keys c > lim of this tile are in the future of this row
         const int lim = row_lim == kNoMask ? kNoMask : row_lim - (key0 + j * BKV);
+        uint32_t see[4] = {0, 0, 0, 0};  // MODE 2, masked tiles: bit c % 32 of word c / 32, key c is seen
+        if constexpr (WN) {
+          const int k0 = ww.key_tile(j) * BKV, t0 = row - lane;  // t0: the warp's first row
+          diag = k0 + BKV - 1 > t0 || (a.window && k0 <= t0 + 31 - a.window && k0 + BKV > a.sinks);
+          if (diag) {
+            const int hi = row + 1 - k0, lo = a.window ? hi - a.window : 0, sk = a.sinks - k0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              see[c] = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+          }
+        }
+        auto seen = [&](int c) { return WN ? ((see[c >> 5] >> (c & 31)) & 1u) != 0 : c <= lim; };
         // pass 1: row maximum of the raw scores (four TMEM loads behind one wait; 3-input
         // max); only the diagonal tile needs the causal mask (a warp-uniform branch)
         float mx = -INFINITY;
@@ -519,7 +619,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (c * 32 + e <= lim) mx = fmaxf(mx, __uint_as_float(v[c][e]));
+                if (seen(c * 32 + e)) mx = fmaxf(mx, __uint_as_float(v[c][e]));
           } else {
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -587,8 +687,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                          sl2v, nmv);
             float p0 = ex2(x2.x), p1 = ex2(x2.y);
             if (diag) {
-              if (c * 32 + 2 * e > lim) p0 = 0.f;
-              if (c * 32 + 2 * e + 1 > lim) p1 = 0.f;
+              if (!seen(c * 32 + 2 * e)) p0 = 0.f;
+              if (!seen(c * 32 + 2 * e + 1)) p1 = 0.f;
             }
             lsum2 = __fadd2_rn(lsum2, make_float2(p0, p1));
             __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
@@ -623,7 +723,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         orow = (bf16*)a.part_o + ps * (size_t)(a.Hq * DH) + (size_t)h * DH;
         if (store) a.part_lse[ps * a.Hq + h] = m_ref + __log2f(l);
       } else {
-        store = row < a.S;
+        store = row < (WN ? ww.len : a.S);
         orow = (bf16*)a.o + (size_t)b * a.o_bstride + (size_t)row * a.o_ld + (size_t)h * DH;
         if (a.lse && store) a.lse[((size_t)b * a.Hq + h) * a.lse_ld + row] = m_ref + __log2f(l);
       }
@@ -676,7 +776,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 template <int DH, int MODE>
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                         int* status, int grid, cudaStream_t s) {
-  constexpr int sm = tca::Cfg<DH>::SMEM + (MODE ? tca::Cfg<DH>::GATHER_BYTES : 0);
+  constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES : 0);
   cudaError_t e = set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
   if (e != cudaSuccess) return e;
   tca::attn_tc_kernel<DH, MODE><<<grid, tca::NTHREADS, sm, s>>>(tq, tk, tv, a, status);
@@ -693,6 +793,8 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
   if (q_rows >= (1LL << 31) || kv_rows >= (1LL << 31)) return cudaErrorInvalidValue;
   const bool ga = a.g_pairoff != nullptr;
   // MODE 1 gathers query rows from q viewed as [B*S*Hq][dh], one-row boxes (q must be dense)
+  const bool win = a.windowed;
+  if (win && (ga || a.window < 0 || a.sinks < 0 || a.sinks > a.S || a.window > a.S)) return cudaErrorInvalidValue;
   if (ga && (a.q_ld != a.Hq * a.dh || a.q_bstride != (long long)a.S * a.q_ld ||
              (long long)a.B * a.S * a.Hq >= (1LL << 31)))
     return cudaErrorInvalidValue;
@@ -706,7 +808,11 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
   if (e != cudaSuccess) return e;
   e = make_tmap_bf16(&tk, a.k, (int)kv_rows, a.Hkv * a.dh, a.kv_ld, tca::BKV);
   if (e != cudaSuccess) return e;
-  e = make_tmap_bf16(&tv, a.v, (int)kv_rows, a.Hkv * a.dh, a.kv_ld, tca::BKV);
+  // V may have a row stride of its own; its sequences are as many rows apart as K's
+  const int v_ld = a.v_ld ? a.v_ld : a.kv_ld;
+  if (v_ld % 8 || (a.v_ld && (a.v_bstride % v_ld || a.v_bstride / v_ld != a.kv_bstride / a.kv_ld)))
+    return cudaErrorInvalidValue;
+  e = make_tmap_bf16(&tv, a.v, (int)kv_rows, a.Hkv * a.dh, v_ld, tca::BKV);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -732,8 +838,12 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
     cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev);
     const double kv_bytes = 2.0 * NS * (double)a.S * a.dh * 2;  // K and V, bf16
     const int want = (8 * grid + G * npairs - 1) / (G * npairs);
-    c.chunk = kv_bytes <= 0.5 * l2 ? NS : (want < 1 ? 1 : (want > NS ? NS : want));
+    // (a window's items run side by side over a few windows of keys: one chunk of all streams)
+    c.chunk = kv_bytes <= 0.5 * l2 || a.window ? NS : (want < 1 ? 1 : (want > NS ? NS : want));
   }
+  if (win)
+    return a.dh == 128 ? launch_attn<128, 2>(tq, tk, tv, c, status, grid, s)
+                       : launch_attn<64, 2>(tq, tk, tv, c, status, grid, s);
   if (a.dh == 128)
     return ga ? launch_attn<128, 1>(tq, tk, tv, c, status, grid, s) : launch_attn<128, 0>(tq, tk, tv, c, status, grid, s);
   return ga ? launch_attn<64, 1>(tq, tk, tv, c, status, grid, s) : launch_attn<64, 0>(tq, tk, tv, c, status, grid, s);

@@ -20,6 +20,14 @@
 // each taking 64 of a row's 128 columns; a warp packs its bf16 results into the first 32 columns of
 // its own 64-column range (so neither half overwrites what the other still reads), and the MMAs
 // read K-step kk (16 columns) at packed column kk * 8 + (kk >= 4 ? 32 : 0).
+//
+// WN (window with sinks, see AttnArgs): position t sees j <= t with j > t - window or j < sinks, over
+// lens[b] rows; gradients leave as bf16.  dQ streams the sink tiles before the window and the window's
+// tiles.  dK/dV of a key tile streams the query tiles whose window reaches it.  A sink is seen by every
+// later query as well: those query tiles are cut into chunks of `far_tiles` which are work items of
+// their own (one CTA would otherwise walk the whole sequence for the sink tile), and the chunks leave
+// float32 partial sums of the sink rows that sink_sum_kernel adds in a fixed order.  Rows at or past
+// lens[b] are cleared in shared memory wherever a product sums over them.
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
@@ -69,8 +77,47 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *(uint32_t*)&h;
 }
 
-// ============================================================================ dQ
+// Clears rows [used, 128) of a swizzled tile (whole warp), ordered before the MMAs issued afterwards.
 template <int DH>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int used, int lane) {
+  for (int i = max(used, 0) * 8 + lane; i < BT * 8; i += 32)  // 16-byte pieces: 8 per 64-column row
+    for (int hb = 0; hb < DH / 64; ++hb) *(uint4*)(tile + hb * BT * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  __syncwarp();
+}
+__device__ __forceinline__ int used_rows(const AttnBwdArgs& a, int b) {
+  return a.lens ? min(max(a.lens[b], 0), a.S) : a.S;
+}
+// 16 bf16 columns to global memory (dst 16-byte aligned; one 32-byte store when a32).
+__device__ __forceinline__ void store_bf16x16(bf16* dst, const uint32_t (&w)[8], bool a32) {
+  if (a32) {
+    st_global_v8(dst, w);
+  } else {
+    *(uint4*)dst = make_uint4(w[0], w[1], w[2], w[3]);
+    *(uint4*)(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// WN: key tiles of query tile qt: n steps, step j at tile j < nsk ? j : lo + j - nsk.
+struct KeyTiles {
+  int lo, nsk, n;
+  __device__ __forceinline__ int tile(int j) const { return j < nsk ? j : lo + j - nsk; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const AttnBwdArgs& a, int qt) {
+  KeyTiles k;
+  k.lo = a.window ? max(0, qt * BT - a.window + 1) / BT : 0;
+  k.nsk = min((a.sinks + BT - 1) / BT, k.lo);
+  k.n = k.nsk + qt - k.lo + 1;
+  return k;
+}
+// WN: last query tile whose window reaches key tile kt, and the far chunks of a sink tile behind it.
+__device__ __forceinline__ int last_query_tile(const AttnBwdArgs& a, int kt, int nqt_used) {
+  if (!a.window) return nqt_used - 1;
+  return min(nqt_used - 1, (kt * BT + BT - 1 + a.window - 1) / BT);
+}
+
+// ============================================================================ dQ
+template <int DH, bool WN>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -149,20 +196,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_prefetch_desc(&tmdO);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
-      int kvit = 0;
+      int kvit = 0, done = 0;
       bool ok = true;
       for (int rr = 0; ok; ++rr) {
         const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
         if (w < 0) break;
         int b, h, qt;
         item(w, b, h, qt);
-        if (!mbar_wait(q_empty, (rr & 1) ^ 1, abort, status)) break;
+        KeyTiles kl;
+        if constexpr (WN) {
+          if (qt * BT >= used_rows(a, b)) continue;  // (every role skips the same items)
+          kl = key_tiles(a, qt);
+        }
+        const int n = WN ? kl.n : qt + 1, it = done++;
+        if (!mbar_wait(q_empty, (it & 1) ^ 1, abort, status)) break;
         mbar_expect_tx(q_full, 2 * C::TILE);
         for (int hb = 0; hb < C::NH; ++hb) {
           tma_load_2d(sQ + hb * C::HALF, &tmQ, q_full, h * DH + hb * 64, b * a.S + qt * BT);
           tma_load_2d(sdO + hb * C::HALF, &tmdO, q_full, h * DH + hb * 64, b * a.S + qt * BT);
         }
-        for (int j = 0; j <= qt; ++j, ++kvit) {
+        for (int j = 0; j < n; ++j, ++kvit) {
+          const int ky = b * a.S + (WN ? kl.tile(j) : j) * BT;
           const int ks = kvit % C::KST, vs = kvit % C::VST;
           if (!mbar_wait(&k_empty[ks], ((kvit / C::KST) & 1) ^ 1, abort, status)) {
             ok = false;
@@ -170,21 +224,36 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           mbar_expect_tx(&k_full[ks], C::TILE);
           for (int hb = 0; hb < C::NH; ++hb)
-            tma_load_2d(sK + ks * C::TILE + hb * C::HALF, &tmK, &k_full[ks], (h / G) * DH + hb * 64, b * a.S + j * BT);
+            tma_load_2d(sK + ks * C::TILE + hb * C::HALF, &tmK, &k_full[ks], (h / G) * DH + hb * 64, ky);
           if (!mbar_wait(&v_empty[vs], ((kvit / C::VST) & 1) ^ 1, abort, status)) {
             ok = false;
             break;
           }
           mbar_expect_tx(&v_full[vs], C::TILE);
           for (int hb = 0; hb < C::NH; ++hb)
-            tma_load_2d(sV + vs * C::TILE + hb * C::HALF, &tmV, &v_full[vs], (h / G) * DH + hb * 64, b * a.S + j * BT);
+            tma_load_2d(sV + vs * C::TILE + hb * C::HALF, &tmV, &v_full[vs], (h / G) * DH + hb * 64, ky);
         }
       }
     }
   } else if (warp == 1) {  // the whole warp runs the MMA role; one elected lane issues
     const uint64_t qd = sdesc_kmajor_sw128(sQ), dod = sdesc_kmajor_sw128(sdO);
-    int kvit = 0, pc = 0, sf = 0;
+    int kvit = 0, pc = 0, sf = 0, done = 0, len = 0;
     bool ok = true, first = true;
+    KeyTiles kl = {};
+    // K (V) of step j has landed in its ring slot; WN clears its rows at or past the sequence's end:
+    // dQ sums over the keys, and dP of such a key would put NaN * 0 into dS
+    auto k_ready = [&](int cur, int j) {
+      if (!mbar_wait_warp(&k_full[cur % C::KST], (cur / C::KST) & 1, abort, status)) return false;
+      if constexpr (WN)
+        if (kl.tile(j) * BT + BT > len) clear_rows<DH>(sK + cur % C::KST * C::TILE, len - kl.tile(j) * BT, lane);
+      return true;
+    };
+    auto v_ready = [&](int cur, int j) {
+      if (!mbar_wait_warp(&v_full[cur % C::VST], (cur / C::VST) & 1, abort, status)) return false;
+      if constexpr (WN)
+        if (kl.tile(j) * BT + BT > len) clear_rows<DH>(sV + cur % C::VST * C::TILE, len - kl.tile(j) * BT, lane);
+      return true;
+    };
     // S = Q K^T for the key tile in K ring slot `st`
     auto issue_s = [&](int st) {
       const uint64_t kd = sdesc_kmajor_sw128(sK + st * C::TILE);
@@ -217,9 +286,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (w < 0) break;
       int b, h, qt;
       item(w, b, h, qt);
-      const int n = qt + 1;
-      if (!mbar_wait_warp(q_full, rr & 1, abort, status)) break;
-      if (!mbar_wait_warp(&k_full[kvit % C::KST], (kvit / C::KST) & 1, abort, status)) break;
+      if constexpr (WN) {
+        len = used_rows(a, b);
+        if (qt * BT >= len) continue;
+        kl = key_tiles(a, qt);
+      }
+      const int n = WN ? kl.n : qt + 1, it = done++;
+      if (!mbar_wait_warp(q_full, it & 1, abort, status)) break;
+      if (!k_ready(kvit, 0)) break;
       if (!first) {
         if (!mbar_wait_warp(s_free, sf & 1, abort, status)) break;
         ++sf;
@@ -227,14 +301,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       first = false;
       tc_fence_after();
       issue_s(kvit % C::KST);
-      if (!mbar_wait_warp(&v_full[kvit % C::VST], (kvit / C::VST) & 1, abort, status)) break;
+      if (!v_ready(kvit, 0)) break;
       tc_fence_after();
       issue_dp(kvit % C::VST);
       if (n == 1) umma_commit_w(q_empty);
       for (int j = 0; j < n; ++j) {
         const int cur = kvit + j, nxt = cur + 1;
         if (j + 1 < n) {
-          if (!mbar_wait_warp(&k_full[nxt % C::KST], (nxt / C::KST) & 1, abort, status)) { ok = false; break; }
+          if (!k_ready(nxt, j + 1)) { ok = false; break; }
           if (!mbar_wait_warp(s_free, sf & 1, abort, status)) { ok = false; break; }
           ++sf;
           tc_fence_after();
@@ -242,12 +316,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!mbar_wait_warp(p_full, pc & 1, abort, status)) { ok = false; break; }
         ++pc;
-        if (j == 0 && !mbar_wait_warp(dq_empty, (rr & 1) ^ 1, abort, status)) { ok = false; break; }
+        if (j == 0 && !mbar_wait_warp(dq_empty, (it & 1) ^ 1, abort, status)) { ok = false; break; }
         tc_fence_after();
         issue_dq(cur % C::KST, j > 0);
         umma_commit_w(&k_empty[cur % C::KST]);
         if (j + 1 < n) {
-          if (!mbar_wait_warp(&v_full[nxt % C::VST], (nxt / C::VST) & 1, abort, status)) { ok = false; break; }
+          if (!v_ready(nxt, j + 1)) { ok = false; break; }
           tc_fence_after();
           issue_dp(nxt % C::VST);
           if (j + 2 == n) umma_commit_w(q_empty);  // Q and dO's last use
@@ -270,14 +344,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t s_tmem = tbase + lane_off + S_COL, p_tmem = tbase + lane_off + P_COL;
     const uint32_t q_tmem = tbase + lane_off + Q_COL + half * (DH / 2);
     const float sl2 = a.scale * 1.4426950408889634f, l2scale = log2f(a.scale);
-    int sit = 0;
+    int sit = 0, done = 0;
     for (int rr = 0;; ++rr) {
       const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
-      int b, h, qt;
+      int b, h, qt, len = a.S;
       item(w, b, h, qt);
-      const int n = qt + 1, row = qt * BT + r;
-      const bool valid = row < a.S;
+      KeyTiles kl;
+      if constexpr (WN) {
+        len = used_rows(a, b);
+        if (qt * BT >= len) continue;
+        kl = key_tiles(a, qt);
+      }
+      const int n = WN ? kl.n : qt + 1, row = qt * BT + r, it = done++;
+      const bool valid = row < len;
       const size_t li = ((size_t)b * a.Hq + h) * a.lse_ld + (valid ? row : 0);
       // scale * P = 2^(s sl2 - lse + log2 scale): dQ's factor scale rides in the exponent
       const float lse2 = (valid ? a.lse[li] : 0.f) - l2scale, drow = valid ? a.dsum[li] : 0.f;
@@ -287,8 +367,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = 0; j < n; ++j, ++sit) {
         if (!mbar_wait_warp(s_full, sit & 1, abort, status)) { ok = false; break; }
         tc_fence_after();
-        const int lim = valid ? row - j * BT : -1;  // keys c > lim are masked (all, for a padding row)
-        const bool diag = __any_sync(0xffffffffu, j == n - 1 || !valid);  // warp-uniform
+        const int k0 = (WN ? kl.tile(j) : j) * BT;
+        const int lim = valid ? row - k0 : -1;  // keys c > lim are masked (all, for a padding row)
+        // WN: keys c <= lo are behind the window and masked too, but for the sinks c < sk
+        const int lo = WN && a.window ? row - a.window - k0 : -1, sk = WN ? a.sinks - k0 : 0;
+        const bool diag = __any_sync(0xffffffffu, (WN ? BT - 1 > lim || (lo >= 0 && sk < BT) : j == n - 1) || !valid);  // warp-uniform
         // phase 1: this half's 64 scores into registers (S's columns are then free for S(j+1)),
         // P = 2^(s sl2 - lse) in float32
         uint32_t sv[2][32];
@@ -307,9 +390,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                          sl2v, nlse2v);
             float p0 = ex2(x2.x), p1 = ex2(x2.y);
             if (diag) {
-              const int k0 = c * 32 + 2 * e;
-              p0 = k0 <= lim ? p0 : 0.f;
-              p1 = k0 + 1 <= lim ? p1 : 0.f;
+              const int c0 = c * 32 + 2 * e;
+              if constexpr (WN) {
+                p0 = c0 <= lim && (c0 > lo || c0 < sk) ? p0 : 0.f;
+                p1 = c0 + 1 <= lim && (c0 + 1 > lo || c0 + 1 < sk) ? p1 : 0.f;
+              } else {
+                p0 = c0 <= lim ? p0 : 0.f;
+                p1 = c0 + 1 <= lim ? p1 : 0.f;
+              }
             }
             sv[cc][2 * e] = __float_as_uint(p0);
             sv[cc][2 * e + 1] = __float_as_uint(p1);
@@ -340,8 +428,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
-      if (!mbar_wait_warp(dq_full, rr & 1, abort, status)) break;
+      if (!mbar_wait_warp(dq_full, it & 1, abort, status)) break;
       tc_fence_after();
+      if constexpr (WN) {
+        bf16* dst = (bf16*)a.dq16 + ((size_t)b * a.S + (valid ? row : 0)) * (size_t)(a.Hq * DH) + (size_t)h * DH +
+                    half * (DH / 2);
+        const bool a32 = ((uintptr_t)a.dq16 & 31) == 0;
+#pragma unroll
+        for (int c = 0; c < DH / 2; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(q_tmem + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = pack2(__uint_as_float(v[16 * e + 2 * k]), __uint_as_float(v[16 * e + 2 * k + 1]));
+            if (valid) store_bf16x16(dst + c + 16 * e, u, a32);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dq_empty);
+        continue;
+      }
       float* dst = a.dq + ((size_t)b * a.S + (valid ? row : 0)) * (size_t)(a.Hq * DH) + (size_t)h * DH +
                    half * (DH / 2);
 #pragma unroll
@@ -373,7 +483,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }
 
 // ============================================================================ dK, dV
-template <int DH>
+template <int DH, bool WN>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -433,7 +543,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr uint32_t S_COL = 0, P_COL = 128, V_COL = 256, K_COL = 256 + DH;  // S^T/P^T, dP^T/dS^T, dV, dK
 
   const int nqt = (a.S + BT - 1) / BT;
-  const int nwork = a.B * a.Hkv * nqt;
+  const int nfar = WN ? a.B * a.Hkv * a.sink_tiles * a.far_chunks : 0;  // WN: far items of the sink tiles come first
+  const int nwork = nfar + a.B * a.Hkv * nqt;
   const int G = a.Hq / a.Hkv;
   // item w: key tile kt (longest first: the most query tiles), KV group g, sequence b; its steps
   // run the G heads (outer) over the query tiles kt..nqt-1 (inner)
@@ -444,6 +555,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     g = rem % a.Hkv;
     b = rem / a.Hkv;
   };
+  // The item with its query tiles [q0, q0 + nq) (nq == 0: nothing to do, every role skips it) and, WN,
+  // its slot among a sink tile's partial sums: 0 for the tile's own item, 1 + chunk for a far one.
+  auto steps = [&](int w, int& b, int& g, int& kt, int& q0, int& nq, int& slot, int& len) {
+    slot = 0;
+    if constexpr (WN) {
+      const bool far = w < nfar;
+      int chunk = 0;
+      if (far) {
+        const int per = a.B * a.Hkv;
+        chunk = w / per / a.sink_tiles;
+        kt = w / per % a.sink_tiles;
+        g = w % per % a.Hkv;
+        b = w % per / a.Hkv;
+        slot = 1 + chunk;
+      } else {
+        item(w - nfar, b, g, kt);
+      }
+      len = used_rows(a, b);
+      const int used = (len + BT - 1) / BT;  // query tiles with rows in use
+      const int last = last_query_tile(a, kt, used);
+      q0 = far ? last + 1 + chunk * a.far_tiles : kt;
+      nq = kt >= used ? 0 : max(0, far ? min(a.far_tiles, used - q0) : last - kt + 1);
+    } else {
+      item(w, b, g, kt);
+      q0 = kt;
+      nq = nqt - kt;
+      len = a.S;
+    }
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -451,22 +591,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_prefetch_desc(&tmdO);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
-      int qdit = 0;
+      int qdit = 0, done = 0;
       bool ok = true;
       for (int rr = 0; ok; ++rr) {
         const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
         if (w < 0) break;
-        int b, g, kt;
-        item(w, b, g, kt);
-        if (!mbar_wait(kv_empty, (rr & 1) ^ 1, abort, status)) break;
+        int b, g, kt, qs, nq, slot, len;
+        steps(w, b, g, kt, qs, nq, slot, len);
+        if (WN && nq == 0) continue;
+        const int it = done++;
+        if (!mbar_wait(kv_empty, (it & 1) ^ 1, abort, status)) break;
         mbar_expect_tx(kv_full, 2 * C::TILE);
         for (int hb = 0; hb < C::NH; ++hb) {
           tma_load_2d(sK + hb * C::HALF, &tmK, kv_full, g * DH + hb * 64, b * a.S + kt * BT);
           tma_load_2d(sV + hb * C::HALF, &tmV, kv_full, g * DH + hb * 64, b * a.S + kt * BT);
         }
-        const int nq = nqt - kt;
         for (int s = 0; s < G * nq; ++s, ++qdit) {
-          const int h = g * G + s / nq, qt = kt + s % nq, st = qdit & 1, ph = ((qdit >> 1) & 1) ^ 1;
+          const int h = g * G + s / nq, qt = qs + s % nq, st = qdit & 1, ph = ((qdit >> 1) & 1) ^ 1;
           if (!mbar_wait(&q_empty[st], ph, abort, status)) {
             ok = false;
             break;
@@ -490,8 +631,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp == 1) {  // the whole warp runs the MMA role; one elected lane issues
     const uint64_t kd = sdesc_kmajor_sw128(sK), vd = sdesc_kmajor_sw128(sV);
-    int qdit = 0, pc = 0, sf = 0;
+    int qdit = 0, pc = 0, sf = 0, done = 0;
     bool ok = true, first = true;
+    int used = BT;  // WN: rows in use of the item's last query tile, cleared behind (dK, dV sum over queries)
+    auto q_ready = [&](int cur, bool end) {
+      if (!mbar_wait_warp(&q_full[cur & 1], (cur >> 1) & 1, abort, status)) return false;
+      if constexpr (WN)
+        if (end && used < BT) clear_rows<DH>(sQ + (cur & 1) * C::QSTAGE, used, lane);
+      return true;
+    };
+    auto do_ready = [&](int cur, bool end) {
+      if (!mbar_wait_warp(&do_full[cur & 1], (cur >> 1) & 1, abort, status)) return false;
+      if constexpr (WN)
+        if (end && used < BT) clear_rows<DH>(sdO + (cur & 1) * C::TILE, used, lane);
+      return true;
+    };
     // S^T = K Q^T for the query stage `st`
     auto issue_s = [&](int st) {
       const uint64_t qd = sdesc_kmajor_sw128(sQ + st * C::QSTAGE);
@@ -534,11 +688,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int rr = 0; ok; ++rr) {
       const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
-      int b, g, kt;
-      item(w, b, g, kt);
-      const int n = G * (nqt - kt);
-      if (!mbar_wait_warp(kv_full, rr & 1, abort, status)) break;
-      if (!mbar_wait_warp(&q_full[qdit & 1], (qdit >> 1) & 1, abort, status)) break;
+      int b, g, kt, qs, nq, slot, len;
+      steps(w, b, g, kt, qs, nq, slot, len);
+      if (WN && nq == 0) continue;
+      const int n = G * nq, it = done++;
+      if constexpr (WN) used = min(BT, len - (qs + nq - 1) * BT);
+      if (!mbar_wait_warp(kv_full, it & 1, abort, status)) break;
+      if (!q_ready(qdit, nq == 1)) break;
       if (!first) {
         if (!mbar_wait_warp(s_free, sf & 1, abort, status)) break;
         ++sf;
@@ -546,13 +702,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       first = false;
       tc_fence_after();
       issue_s(qdit & 1);
-      if (!mbar_wait_warp(&do_full[qdit & 1], (qdit >> 1) & 1, abort, status)) break;
+      if (!do_ready(qdit, nq == 1)) break;
       tc_fence_after();
       issue_dp(qdit & 1);
       for (int s = 0; s < n; ++s) {
-        const int cur = qdit + s, st = cur & 1, nst = (cur + 1) & 1, nph = ((cur + 1) >> 1) & 1;
+        const int cur = qdit + s, st = cur & 1, nst = (cur + 1) & 1;
+        const bool end = WN && (s + 1) % nq == nq - 1;  // step s + 1 takes the item's last query tile
         if (s + 1 < n) {
-          if (!mbar_wait_warp(&q_full[nst], nph, abort, status)) { ok = false; break; }
+          if (!q_ready(cur + 1, end)) { ok = false; break; }
           if (!mbar_wait_warp(s_free, sf & 1, abort, status)) { ok = false; break; }
           ++sf;
           tc_fence_after();
@@ -560,11 +717,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!mbar_wait_warp(p_full, pc & 1, abort, status)) { ok = false; break; }
         ++pc;
-        if (s == 0 && !mbar_wait_warp(acc_empty, (rr & 1) ^ 1, abort, status)) { ok = false; break; }
+        if (s == 0 && !mbar_wait_warp(acc_empty, (it & 1) ^ 1, abort, status)) { ok = false; break; }
         tc_fence_after();
         issue_acc(st, s > 0);
         if (s + 1 < n) {
-          if (!mbar_wait_warp(&do_full[nst], nph, abort, status)) { ok = false; break; }
+          if (!do_ready(cur + 1, end)) { ok = false; break; }
           tc_fence_after();
           issue_dp(nst);
         }
@@ -586,16 +743,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_tmem = tbase + lane_off + S_COL, p_tmem = tbase + lane_off + P_COL;
     const float sl2 = a.scale * 1.4426950408889634f;
-    int sit = 0;
+    int sit = 0, done = 0;
     for (int rr = 0;; ++rr) {
       const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
-      int b, g, kt;
-      item(w, b, g, kt);
-      const int nq = nqt - kt, n = G * nq, key = kt * BT + r;
+      int b, g, kt, qs, nq, slot, len;
+      steps(w, b, g, kt, qs, nq, slot, len);
+      if (WN && nq == 0) continue;
+      const int n = G * nq, key = kt * BT + r, it = done++;
+      // WN: queries at or past this position do not see the key
+      const int until = WN && a.window && key >= a.sinks ? min(len, key + a.window) : len;
       bool ok = true;
       for (int s = 0; s < n; ++s, ++sit) {
-        const int qt = kt + s % nq, st = sit & 1;
+        const int qt = qs + s % nq, st = sit & 1;
         // the stage's lse and D rows: landed with its Q (the stage is not refilled before this
         // step's dK MMAs, which wait for this warp)
         if (!mbar_wait_warp(&q_full[st], (sit >> 1) & 1, abort, status)) { ok = false; break; }
@@ -604,7 +764,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float* lse2 = (const float*)(sQ + st * C::QSTAGE + C::TILE);
         const float* dsum = lse2 + BT;
         // query column c is used iff it is a real row at or after this key: q0 + c < S, q0 + c >= key
-        const int q0 = qt * BT, cmax = a.S - q0, cmin = key - q0;
+        const int q0 = qt * BT, cmax = until - q0, cmin = key - q0;
         const bool masked = __any_sync(0xffffffffu, cmin > 64 * half || cmax < 64 * half + 64);  // warp-uniform
         const float2 sl2v = make_float2(sl2, sl2);
         // phase 1: this half's 64 scores into registers (S^T's columns are then free for the next
@@ -673,9 +833,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
-      if (!mbar_wait_warp(acc_full, rr & 1, abort, status)) break;
+      if (!mbar_wait_warp(acc_full, it & 1, abort, status)) break;
       tc_fence_after();
-      const bool valid = key < a.S;
+      const bool valid = key < len;
+      if constexpr (WN) {
+        // the first warpgroup writes dK = scale * sum dS^T Q, the second dV; sinks of a window leave
+        // float32 partial sums
+        const bool part = a.far_chunks > 0 && key < a.sinks;
+        const uint32_t src = tbase + lane_off + (half ? V_COL : K_COL);
+        const float f = half ? 1.f : a.scale;
+        bf16* d16 = (bf16*)(half ? a.dv16 : a.dk16) + ((size_t)b * a.S + (valid ? key : 0)) * (size_t)(a.Hkv * DH) +
+                    (size_t)g * DH;
+        float* d32 = a.sink_part + ((((size_t)b * a.Hkv + g) * (1 + a.far_chunks) + slot) * a.sinks + (part ? key : 0)) * (2 * DH) +
+                     half * DH;
+        const bool a32 = (((uintptr_t)a.dk16 | (uintptr_t)a.dv16) & 31) == 0;
+#pragma unroll
+        for (int c = 0; c < DH; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(src + c, v);
+          tmem_ld_wait();
+          if (valid && part) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *(float4*)(d32 + c + 4 * e) = make_float4(__uint_as_float(v[4 * e]) * f, __uint_as_float(v[4 * e + 1]) * f,
+                                                        __uint_as_float(v[4 * e + 2]) * f, __uint_as_float(v[4 * e + 3]) * f);
+          } else if (valid && slot == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t u[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                u[k] = pack2(__uint_as_float(v[16 * e + 2 * k]) * f, __uint_as_float(v[16 * e + 2 * k + 1]) * f);
+              store_bf16x16(d16 + c + 16 * e, u, a32);
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        continue;
+      }
       const int wkv = 2 * a.Hkv * DH;
       float* dst = a.dkv + ((size_t)b * a.S + (valid ? key : 0)) * (size_t)wkv + (size_t)g * DH;
       {  // the first warpgroup writes dK (columns [0, dkv)) = scale * sum dS^T Q, the second dV ([dkv, 2 dkv))
@@ -713,20 +911,65 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
+// WN: dK and dV of the sinks = the sum of their partial rows, own item first, then the far chunks in
+// order.  One block per (sink, KV group, sequence), one thread per column of [dK | dV].
+__global__ void sink_sum_kernel(AttnBwdArgs a) {
+  const int key = blockIdx.x, g = blockIdx.y, b = blockIdx.z, c = threadIdx.x;
+  const int len = used_rows(a, b);
+  if (key >= len) return;
+  const int used = (len + BT - 1) / BT, last = last_query_tile(a, key / BT, used);
+  const int n = 1 + (used - 1 - last + a.far_tiles - 1) / a.far_tiles;
+  const float* p = a.sink_part + (((size_t)b * a.Hkv + g) * (1 + a.far_chunks) * a.sinks + key) * (2 * a.dh) + c;
+  float acc = 0.f;
+  for (int i = 0; i < n; ++i) acc += p[(size_t)i * a.sinks * 2 * a.dh];
+  const size_t at = ((size_t)b * a.S + key) * (size_t)(a.Hkv * a.dh) + (size_t)g * a.dh;
+  if (c < a.dh) ((bf16*)a.dk16)[at + c] = __float2bfloat16_rn(acc);
+  else ((bf16*)a.dv16)[at + c - a.dh] = __float2bfloat16_rn(acc);
+}
+
+// WN: dsum[(b * Hq + h) * ld + t] = sum_i dO * O over head h of token t, 0 for t >= lens[b] up to ld.
+// A warp per (token, 32 pieces of 16 bytes): 2 (d_head 128) or 4 heads; any row strides.
+__global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
+                                                          const bf16* __restrict__ o, int ld_o, AttnBwdArgs a,
+                                                          float* __restrict__ dsum) {
+  const int lane = threadIdx.x & 31, per = a.dh / 8, pieces = a.Hq * per;
+  const long long tok = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (tok >= (long long)a.B * a.lse_ld) return;
+  const int b = (int)(tok / a.lse_ld), t = (int)(tok % a.lse_ld);
+  const bool in = t < used_rows(a, b);
+  const uint4* x = (const uint4*)(dout + ((size_t)b * a.S + t) * (size_t)ld_do);
+  const uint4* y = (const uint4*)(o + ((size_t)b * a.S + t) * (size_t)ld_o);
+  for (int p = lane; p - lane < pieces; p += 32) {
+    float acc = 0.f;
+    if (in && p < pieces) {
+      const uint4 u = x[p], v = y[p];
+      const __nv_bfloat162* u2 = (const __nv_bfloat162*)&u;
+      const __nv_bfloat162* v2 = (const __nv_bfloat162*)&v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 fu = __bfloat1622float2(u2[e]), fv = __bfloat1622float2(v2[e]);
+        acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
+      }
+    }
+    for (int k = per / 2; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
+    if (lane % per == 0 && p < pieces) dsum[((size_t)b * a.Hq + p / per) * a.lse_ld + t] = acc;
+  }
+}
+
 }  // namespace tcb
 
-template <int DH>
+template <int DH, bool WN>
 static cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                               const CUtensorMap& tv, const AttnBwdArgs& a, int* status, int sms, cudaStream_t s) {
   using C = tcb::Cfg<DH>;
   const int nqt = (a.S + tcb::BT - 1) / tcb::BT;
-  cudaError_t e = set_max_smem(tcb::attn_bwd_dkdv_kernel<DH>, C::SMEM_DKDV, s);
+  cudaError_t e = set_max_smem(tcb::attn_bwd_dkdv_kernel<DH, WN>, C::SMEM_DKDV, s);
   if (e != cudaSuccess) return e;
-  const int nkv = a.B * a.Hkv * nqt, nq = a.B * a.Hq * nqt;
-  tcb::attn_bwd_dkdv_kernel<DH><<<nkv < sms ? nkv : sms, tcb::NTHREADS, C::SMEM_DKDV, s>>>(tq, tdo, tk, tv, a, status);
+  const int nkv = a.B * a.Hkv * (nqt + (WN ? a.sink_tiles * a.far_chunks : 0)), nq = a.B * a.Hq * nqt;
+  tcb::attn_bwd_dkdv_kernel<DH, WN><<<nkv < sms ? nkv : sms, tcb::NTHREADS, C::SMEM_DKDV, s>>>(tq, tdo, tk, tv, a, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = set_max_smem(tcb::attn_bwd_dq_kernel<DH>, C::SMEM_DQ, s)) != cudaSuccess) return e;
-  tcb::attn_bwd_dq_kernel<DH><<<nq < sms ? nq : sms, tcb::NTHREADS, C::SMEM_DQ, s>>>(tq, tdo, tk, tv, a, status);
+  if ((e = set_max_smem(tcb::attn_bwd_dq_kernel<DH, WN>, C::SMEM_DQ, s)) != cudaSuccess) return e;
+  tcb::attn_bwd_dq_kernel<DH, WN><<<nq < sms ? nq : sms, tcb::NTHREADS, C::SMEM_DQ, s>>>(tq, tdo, tk, tv, a, status);
   return cudaGetLastError();
 }
 
@@ -746,8 +989,62 @@ cudaError_t attention_backward_tc(const AttnBwdArgs& a, int* status, cudaStream_
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return a.dh == 128 ? launch_bwd<128>(tq, tdo, tk, tv, a, status, sms, s)
-                     : launch_bwd<64>(tq, tdo, tk, tv, a, status, sms, s);
+  return a.dh == 128 ? launch_bwd<128, false>(tq, tdo, tk, tv, a, status, sms, s)
+                     : launch_bwd<64, false>(tq, tdo, tk, tv, a, status, sms, s);
+}
+
+// The far chunks of a windowed backward: length in query tiles and the most that a sequence of S rows
+// has.  A chunk is as long as a key tile's own query range, or a 64th of the sequence where that is
+// more: the items stay of one size, and the partial sums within 65 slots per sink row.
+static void far_chunks(AttnBwdArgs& a) {
+  const int nqt = (a.S + tcb::BT - 1) / tcb::BT;
+  a.sink_tiles = a.far_chunks = 0;
+  a.far_tiles = 1;
+  if (!a.window || !a.sinks) return;
+  const int reach = (tcb::BT - 1 + a.window - 1) / tcb::BT;  // last query tile of key tile 0
+  if (reach >= nqt - 1) return;
+  a.far_tiles = reach + 1 > (nqt + 63) / 64 ? reach + 1 : (nqt + 63) / 64;
+  a.sink_tiles = (a.sinks + tcb::BT - 1) / tcb::BT;
+  a.far_chunks = (nqt - 1 - reach + a.far_tiles - 1) / a.far_tiles;
+}
+
+size_t window_attention_backward_scratch(int B, int S, int Hq, int Hkv, int dh, int window, int sinks, size_t* part) {
+  AttnBwdArgs a = {};
+  a.S = S; a.window = window; a.sinks = sinks;
+  far_chunks(a);
+  const size_t d = ((size_t)B * Hq * ((S + 127) / 128 * 128) * 4 + 255) / 256 * 256;
+  if (part) *part = d;
+  return d + (a.far_chunks ? (size_t)B * Hkv * (1 + a.far_chunks) * sinks * 2 * dh * 4 : 0);
+}
+
+cudaError_t window_attention_backward_tc(const AttnBwdArgs& args, const AttnBwdStrides& ld, const void* o, float* dsum,
+                                         int* status, cudaStream_t s) {
+  AttnBwdArgs a = args;
+  if (a.B <= 0 || a.S <= 0) return cudaSuccess;
+  if ((a.dh != 64 && a.dh != 128) || a.Hq % a.Hkv || a.lse_ld < (a.S + tcb::BT - 1) / tcb::BT * tcb::BT || a.window < 0 ||
+      a.sinks < 0 || a.sinks > a.S || a.window > a.S || (long long)a.B * a.S >= (1LL << 31))
+    return cudaErrorInvalidValue;
+  far_chunks(a);
+  a.dsum = dsum;
+  const long long warps = (long long)a.B * a.lse_ld;
+  tcb::window_dsum_kernel<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>((const bf16*)a.dout, ld.dout, (const bf16*)o,
+                                                                               ld.o, a, dsum);
+  cudaError_t e = cudaGetLastError();
+  CUtensorMap tq, tdo, tk, tv;
+  const int rows = a.B * a.S;
+  if (e == cudaSuccess) e = make_tmap_bf16(&tq, a.q, rows, a.Hq * a.dh, ld.q, tcb::BT);
+  if (e == cudaSuccess) e = make_tmap_bf16(&tdo, a.dout, rows, a.Hq * a.dh, ld.dout, tcb::BT);
+  if (e == cudaSuccess) e = make_tmap_bf16(&tk, a.k, rows, a.Hkv * a.dh, ld.k, tcb::BT);
+  if (e == cudaSuccess) e = make_tmap_bf16(&tv, a.v, rows, a.Hkv * a.dh, ld.v, tcb::BT);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  e = a.dh == 128 ? launch_bwd<128, true>(tq, tdo, tk, tv, a, status, sms, s)
+                  : launch_bwd<64, true>(tq, tdo, tk, tv, a, status, sms, s);
+  if (e != cudaSuccess || !a.far_chunks) return e;
+  tcb::sink_sum_kernel<<<dim3(a.sinks, a.Hkv, a.B), 2 * a.dh, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace mka
