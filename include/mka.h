@@ -285,6 +285,79 @@ MKA_API int mka_window_attention_backward(const mka_attn_config* cfg, const mka_
                                           const void* dout, const int32_t* lens, void* dq, void* dk, void* dv, void* ws,
                                           size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ K/V cache in 8 bits
+ * A K/V cache of half the bytes of a bf16 one, for decoding over long contexts, and its thinning.
+ * Caller-owned device buffers, laid out as
+ *   k, v             [B, Hkv, max_positions, dh]  e4m3 codes, one byte each
+ *   k_scale, v_scale [B, Hkv, ceil(max_positions / block)]  float32 powers of two
+ * The value of a code at position j is code * scale[j / block].  A block's scale is the smallest power
+ * of two s >= 2^-120 with |value| <= 448 s for all of its values (448: the largest e4m3 value), and
+ * values are rounded to the nearest code (ties to even): to 2^-4 of the value, or 2^-10 of the block's
+ * scale where that is more.  NaN and infinities are stored as NaN and do not enter the scale.  The
+ * calls keep no lengths: every call is told the positions in use, in device memory, so sequences of
+ * steps can be captured into a CUDA graph.  Position arrays hold int32 on the device. */
+typedef struct mka_kv8_config {
+  int32_t batch;         /* B */
+  int32_t max_positions; /* rows of the cache per sequence and head */
+  int32_t n_q_heads;     /* Hq, a multiple of n_kv_heads; query head h reads KV head h / (Hq / Hkv) */
+  int32_t n_kv_heads;    /* Hkv */
+  int32_t d_head;        /* 64 or 128 */
+  int32_t block;         /* positions that share a scale: 16, 32, 64 or 128 */
+  int32_t dtype;         /* mka_dtype_t of the rows that go in and come out (q, out, K/V rows) */
+  int32_t window;        /* as in mka_attn_config, over cache positions */
+  int32_t sinks;
+  float attn_scale;      /* <= 0 selects 1/sqrt(d_head) */
+} mka_kv8_config;
+typedef struct mka_kv8_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} mka_kv8_cache;
+
+/* Write count[b] (NULL: n) of the n rows of k_new, v_new (dtype) of every sequence b to its positions
+ * pos[b] .. pos[b] + count[b] - 1.  Row t of sequence b, head g starts at element
+ * b * batch_stride + t * row_stride + g * dh (strides in elements, multiples of 16 bytes).  A block that
+ * already holds rows in front of pos[b] keeps them, and its scale does not shrink: where it grows, the
+ * older codes are rounded to the new scale.  Rows behind the new ones do not count, whatever they hold.
+ * A sequence whose rows do not fit records MKA_ERR_CAPACITY (a negative position MKA_ERR_DEVICE_BOUNDS)
+ * in the status word and is left as it was. */
+MKA_API int mka_kv8_append(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const void* k_new, const void* v_new,
+                           int64_t row_stride, int64_t batch_stride, int32_t n, const int32_t* pos, const int32_t* count,
+                           void* stream);
+/* Values (dtype) of positions first[b] (NULL: 0) .. first[b] + rows[b] - 1 (rows NULL: n; clamped to
+ * [0, n]) to rows 0.. of k_out, v_out, addressed like k_new of mka_kv8_append; other rows are left as
+ * they were.  A range outside the cache records MKA_ERR_DEVICE_BOUNDS and reads nothing. */
+MKA_API int mka_kv8_read(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const int32_t* first, const int32_t* rows,
+                         int32_t n, void* k_out, void* v_out, int64_t row_stride, int64_t batch_stride, void* stream);
+/* Bytes of scratch for mka_kv8_attention with n new tokens (0 on a bad cfg). */
+MKA_API size_t mka_kv8_attention_workspace_size(const mka_kv8_config* cfg, int32_t n, int32_t with_weights);
+/* Attention of the last n positions of every sequence over its cache (their K/V appended before):
+ * query i of sequence b stands at position p = lens[b] - n + i and sees j <= p within window and sinks.
+ * q, out [B, n, Hq*dh] (dtype, dense).  A query without a position (p < 0) gives 0.  lens is clamped to
+ * [0, max_positions]; positions at or past it, and hidden ones, reach no result, whatever they hold.
+ * weights (nullable) [B, Hkv, max_positions] float32: position j gets the softmax weight that the n
+ * queries of the Hq / Hkv heads of its KV head gave it added; hidden positions are left as they were.
+ * Scores, softmax and sums are float32; probabilities enter the product with V rounded to half
+ * precision relative to the row's largest (float32 rows: to twice that many bits).
+ * ws: 16-byte aligned scratch, used by one call at a time. */
+MKA_API int mka_kv8_attention(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const void* q, int32_t n,
+                              const int32_t* lens, void* out, float* weights, void* ws, size_t ws_bytes, void* stream);
+/* Thin a cache: per sequence and KV head keep `keep` positions -- the first `first`, the last `recent`
+ * and, of those between, the ones with the largest weights (ties to the lowest position, NaN above all)
+ * -- and write them in order to dst, requantised into its blocks.  A sequence of at most `keep`
+ * positions keeps them all.  weights [B, Hkv, cfg->max_positions]; lens [B] (clamped).  dst_cfg and dst:
+ * another cache of the same batch, KV heads and head size with max_positions >= keep.  Outputs:
+ * dst_lens [B] = min(lens[b], keep); dst_weights (nullable) [B, Hkv, dst_cfg->max_positions], the kept
+ * weights; kept [B, Hkv, keep] int32, the kept positions, -1 past the last.  Rows of dst behind
+ * dst_lens[b] are left as they were.  first + recent <= keep.
+ * ws: mka_kv8_evict_workspace_size bytes, 16-byte aligned, used by one call at a time. */
+MKA_API size_t mka_kv8_evict_workspace_size(const mka_kv8_config* cfg, int32_t keep);
+MKA_API int mka_kv8_evict(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const int32_t* lens, const float* weights,
+                          int32_t keep, int32_t first, int32_t recent, const mka_kv8_config* dst_cfg,
+                          const mka_kv8_cache* dst, int32_t* dst_lens, float* dst_weights, int32_t* kept, void* ws,
+                          size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ without caller scratch */
 
 /* Bytes of the library's built-in scratch used by mka_session_ema_noalloc. */

@@ -44,6 +44,8 @@ EXPORTED = [
     "mka_session_ema_noalloc", "mka_selftest_wait_timeout", "mka_train_workspace_size", "mka_prefill_forward_train",
     "mka_prefill_backward", "mka_set_wait_limit", "mka_window_attention",
     "mka_window_attention_backward_workspace_size", "mka_window_attention_backward",
+    "mka_kv8_append", "mka_kv8_read", "mka_kv8_attention_workspace_size", "mka_kv8_attention",
+    "mka_kv8_evict_workspace_size", "mka_kv8_evict",
 ]
 
 
@@ -71,6 +73,16 @@ class mka_attn_strides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("q", "k", "v", "out", "dout")]
 
 
+class mka_kv8_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "max_positions", "n_q_heads", "n_kv_heads", "d_head", "block",
+                                              "dtype", "window", "sinks")] + [("attn_scale", ctypes.c_float)]
+
+
+class mka_kv8_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+
+
+_kcp, _kvp, _i64 = ctypes.POINTER(mka_kv8_config), ctypes.POINTER(mka_kv8_cache), ctypes.c_int64
 _acp, _asp = ctypes.POINTER(mka_attn_config), ctypes.POINTER(mka_attn_strides)
 _vp, _sz, _i32, _cfgp = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.POINTER(mka_config)
 _SIGS = {
@@ -103,6 +115,12 @@ _SIGS = {
     "mka_window_attention": (ctypes.c_int, [_acp, _asp] + [_vp] * 7),
     "mka_window_attention_backward_workspace_size": (_sz, [_acp]),
     "mka_window_attention_backward": (ctypes.c_int, [_acp, _asp] + [_vp] * 11 + [_sz, _vp]),
+    "mka_kv8_append": (ctypes.c_int, [_kcp, _kvp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "mka_kv8_read": (ctypes.c_int, [_kcp, _kvp, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp]),
+    "mka_kv8_attention_workspace_size": (_sz, [_kcp, _i32, _i32]),
+    "mka_kv8_attention": (ctypes.c_int, [_kcp, _kvp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mka_kv8_evict_workspace_size": (_sz, [_kcp, _i32]),
+    "mka_kv8_evict": (ctypes.c_int, [_kcp, _kvp, _vp, _vp, _i32, _i32, _i32, _kcp, _kvp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -338,6 +356,112 @@ def mka_window_attention_backward(c: mka_attn_config, q, k, v, out, lse, dout, l
         _dense(lens, "lens", torch.int32, B), _dense(dq, "dq", bf, B, S, H * d), _dense(dk, "dk", bf, B, S, G * d),
         _dense(dv, "dv", bf, B, S, G * d), ws.data_ptr(), ws.numel() * ws.element_size(), s),
         "mka_window_attention_backward")
+
+
+def make_kv8_config(batch: int, max_positions: int, n_q_heads: int, n_kv_heads: int, d_head: int, block: int = 64,
+                    dtype: str = "bf16", window: int = 0, sinks: int = 0,
+                    attn_scale: Optional[float] = None) -> mka_kv8_config:
+    """Shape of an 8-bit cache and of the attention over it."""
+    return mka_kv8_config(batch=batch, max_positions=max_positions, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads,
+                          d_head=d_head, block=block, dtype={"f32": MKA_F32, "bf16": MKA_BF16}[dtype], window=window,
+                          sinks=sinks, attn_scale=attn_scale or 0.0)
+
+
+def kv8_cache(k, v, k_scale, v_scale) -> mka_kv8_cache:
+    """The cache made of these tensors: codes [B, Hkv, max_positions, dh] (float8_e4m3fn or uint8) and scales
+    [B, Hkv, ceil(max_positions / block)] float32, contiguous.  Keeps the tensors alive."""
+    for t in (k, v, k_scale, v_scale):
+        if not t.is_contiguous():
+            raise ValueError("the tensors of an 8-bit cache must be contiguous")
+    if k.dtype not in (torch.uint8, torch.float8_e4m3fn) or v.dtype != k.dtype or k.shape != v.shape or k.dim() != 4:
+        raise ValueError("codes must be [B, Hkv, max_positions, dh] of float8_e4m3fn or uint8")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != v_scale.shape or k_scale.dim() != 3:
+        raise ValueError("scales must be [B, Hkv, blocks] of float32")
+    x = mka_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    x.tensors = (k, v, k_scale, v_scale)
+    return x
+
+
+def _check_cache(c: mka_kv8_config, x: mka_kv8_cache) -> None:
+    k, _, s, _ = x.tensors
+    if k.shape != (c.batch, c.n_kv_heads, c.max_positions, c.d_head):
+        raise ValueError(f"the cache's codes are {tuple(k.shape)}, not what the configuration says")
+    if c.block > 0 and s.shape != (c.batch, c.n_kv_heads, -(-c.max_positions // c.block)):
+        raise ValueError(f"the cache's scales are {tuple(s.shape)}, not what the configuration says")
+
+
+def _kv_rows(c: mka_kv8_config, t: torch.Tensor, name: str):
+    """(rows, row stride, batch stride) of K/V rows [B, n, Hkv, dh] or [B, n, Hkv * dh]."""
+    _dtype(t, torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32, name)
+    width = c.n_kv_heads * c.d_head
+    n = t.shape[1] if t.dim() in (3, 4) else -1
+    if t.shape not in ((c.batch, n, c.n_kv_heads, c.d_head), (c.batch, n, width)):
+        raise ValueError(f"{name} must be [{c.batch}, n, {c.n_kv_heads}, {c.d_head}], not {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 or (t.dim() == 4 and c.n_kv_heads > 1 and st[2] != c.d_head):
+        raise ValueError(f"{name}: the elements of a row must be contiguous, strides {st}")
+    return n, (st[1] if n > 1 else width), (st[0] if c.batch > 1 else 0)
+
+
+def mka_kv8_append(c: mka_kv8_config, cache: mka_kv8_cache, k_new, v_new, pos, count=None, stream=None) -> None:
+    """k_new, v_new [B, n, Hkv, dh] of the configuration's type (row and batch strides allowed, the same for both);
+    pos, count [B] int32 on the device."""
+    s = _call_stream((k_new, v_new, pos, count) + cache.tensors, stream)
+    _check_cache(c, cache)
+    rows = _kv_rows(c, k_new, "k_new")
+    if _kv_rows(c, v_new, "v_new") != rows:
+        raise ValueError("k_new and v_new must have the same shape and strides")
+    _check(_lib.mka_kv8_append(c, cache, k_new.data_ptr(), v_new.data_ptr(), rows[1], rows[2], rows[0],
+                               _dense(pos, "pos", torch.int32, c.batch), _dense(count, "count", torch.int32, c.batch), s),
+           "mka_kv8_append")
+
+
+def mka_kv8_read(c: mka_kv8_config, cache: mka_kv8_cache, first, rows, k_out, v_out, stream=None) -> None:
+    """Values of positions first[b] .. first[b] + rows[b] - 1 to k_out, v_out [B, n, Hkv, dh] (strides allowed)."""
+    s = _call_stream((first, rows, k_out, v_out) + cache.tensors, stream)
+    _check_cache(c, cache)
+    at = _kv_rows(c, k_out, "k_out")
+    if _kv_rows(c, v_out, "v_out") != at:
+        raise ValueError("k_out and v_out must have the same shape and strides")
+    _check(_lib.mka_kv8_read(c, cache, _dense(first, "first", torch.int32, c.batch),
+                             _dense(rows, "rows", torch.int32, c.batch), at[0], k_out.data_ptr(), v_out.data_ptr(), at[1],
+                             at[2], s), "mka_kv8_read")
+
+
+def mka_kv8_attention_workspace_size(c: mka_kv8_config, n: int = 1, with_weights: bool = False) -> int:
+    return _lib.mka_kv8_attention_workspace_size(c, n, 1 if with_weights else 0)
+
+
+def mka_kv8_attention(c: mka_kv8_config, cache: mka_kv8_cache, q, lens, out, weights, ws, stream=None) -> None:
+    """Attention of the last n positions: q, out [B, n, Hq, dh] (or flat heads), dense; lens [B] int32 on the device;
+    weights [B, Hkv, max_positions] float32 or None."""
+    s = _call_stream((q, lens, out, weights, ws) + cache.tensors, stream)
+    _check_cache(c, cache)
+    dt = torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32
+    n = q.shape[1] if q.dim() >= 2 else 0
+    _check(_lib.mka_kv8_attention(
+        c, cache, _dense(q, "q", dt, c.batch, n, c.n_q_heads * c.d_head), n, _dense(lens, "lens", torch.int32, c.batch),
+        _dense(out, "out", dt, c.batch, n, c.n_q_heads * c.d_head),
+        _dense(weights, "weights", torch.float32, c.batch, c.n_kv_heads, c.max_positions), ws.data_ptr(),
+        ws.numel() * ws.element_size(), s), "mka_kv8_attention")
+
+
+def mka_kv8_evict_workspace_size(c: mka_kv8_config, keep: int) -> int:
+    return _lib.mka_kv8_evict_workspace_size(c, keep)
+
+
+def mka_kv8_evict(c: mka_kv8_config, cache: mka_kv8_cache, lens, weights, keep: int, first: int, recent: int,
+                  dst_c: mka_kv8_config, dst: mka_kv8_cache, dst_lens, dst_weights, kept, ws, stream=None) -> None:
+    """Keeps `keep` positions of every sequence and KV head (the first, the last, the heaviest) in another cache."""
+    s = _call_stream((lens, weights, dst_lens, dst_weights, kept, ws) + cache.tensors + dst.tensors, stream)
+    _check_cache(c, cache)
+    _check_cache(dst_c, dst)
+    B, H = c.batch, c.n_kv_heads
+    _check(_lib.mka_kv8_evict(
+        c, cache, _dense(lens, "lens", torch.int32, B), _dense(weights, "weights", torch.float32, B, H, c.max_positions),
+        keep, first, recent, dst_c, dst, _dense(dst_lens, "dst_lens", torch.int32, B),
+        _dense(dst_weights, "dst_weights", torch.float32, B, H, dst_c.max_positions),
+        _dense(kept, "kept", torch.int32, B, H, keep), ws.data_ptr(), ws.numel() * ws.element_size(), s), "mka_kv8_evict")
 
 
 def mka_status() -> int:

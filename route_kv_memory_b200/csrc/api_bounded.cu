@@ -82,9 +82,168 @@ int check_win(const char* who, const mka_attn_config* c, const mka_attn_strides*
   return MKA_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit cache
+struct Kv {
+  Kv8Args a;
+  int Hq, G, bf16, window, sinks;
+  float scale;
+};
+int check_kv8(const char* who, const mka_kv8_config* c, const mka_kv8_cache* cache, Kv* o) {
+  if (!c) return fail(MKA_ERR_INVALID_ARG, "%s: cfg is NULL", who);
+  if (c->batch < 1 || c->max_positions < 1) return fail(MKA_ERR_INVALID_ARG, "%s: batch and max_positions must be >= 1", who);
+  const int e = check_heads(who, c->n_q_heads, c->n_kv_heads, c->d_head, c->attn_scale, &o->scale);
+  if (e != MKA_OK) return e;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
+    return fail(MKA_ERR_UNSUPPORTED, "%s: block must be 16, 32, 64 or 128", who);
+  if (c->dtype != MKA_F32 && c->dtype != MKA_BF16) return fail(MKA_ERR_INVALID_ARG, "%s: dtype must be MKA_F32 or MKA_BF16", who);
+  if (c->window < 0 || c->sinks < 0) return fail(MKA_ERR_INVALID_ARG, "%s: window and sinks must be >= 0", who);
+  if (c->batch > 65535 || c->n_kv_heads > 32767 || c->max_positions > (1 << 28) ||
+      (long long)c->n_q_heads * c->d_head > (1LL << 24) || (long long)c->batch * c->n_kv_heads > (1 << 20) ||
+      (long long)c->batch * c->n_kv_heads * c->max_positions > (1LL << 36))
+    return fail(MKA_ERR_UNSUPPORTED, "%s: batch, heads or max_positions too large", who);
+  o->a = {nullptr, nullptr, nullptr, nullptr, c->batch, c->n_kv_heads, c->d_head, c->max_positions, c->block,
+          (c->max_positions + c->block - 1) / c->block};
+  o->Hq = c->n_q_heads;
+  o->G = c->n_q_heads / c->n_kv_heads;
+  o->bf16 = c->dtype == MKA_BF16;
+  o->window = c->window >= c->max_positions ? 0 : c->window;
+  o->sinks = o->window ? (c->sinks < c->max_positions ? c->sinks : c->max_positions) : 0;
+  if (cache) {
+    NEED(cache->k); NEED(cache->v);
+    if (!cache->k_scale || !cache->v_scale || ((uintptr_t)cache->k_scale & 3) || ((uintptr_t)cache->v_scale & 3))
+      return fail(MKA_ERR_INVALID_ARG, "%s: a scale pointer is NULL or misaligned", who);
+    o->a.k = cache->k; o->a.v = cache->v; o->a.ks = cache->k_scale; o->a.vs = cache->v_scale;
+  }
+  return MKA_OK;
+}
+int check_positions(const char* who, const int32_t* p, const char* name, bool needed) {
+  if (needed && !p) return fail(MKA_ERR_INVALID_ARG, "%s: %s is NULL", who, name);
+  if ((uintptr_t)p & 3) return fail(MKA_ERR_INVALID_ARG, "%s: %s is not aligned", who, name);
+  return MKA_OK;
+}
+int check_rows(const char* who, const Kv& kv, int64_t row_stride, int64_t batch_stride, int32_t n) {
+  const int per = kv.bf16 ? 8 : 4;  // elements of 16 bytes
+  if (n < 1) return fail(MKA_ERR_INVALID_ARG, "%s: n must be >= 1", who);
+  if (row_stride < (int64_t)kv.a.Hkv * kv.a.dh || row_stride % per || batch_stride < 0 || batch_stride % per)
+    return fail(MKA_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes, rows at least n_kv_heads * d_head apart", who);
+  if ((int64_t)n * kv.a.Hkv * (kv.a.dh / 16) > 0x7fffff00) return fail(MKA_ERR_UNSUPPORTED, "%s: n too large", who);
+  return MKA_OK;
+}
+// Attention limits: grid dimensions and the flat count of 128-position tiles.
+int check_kv8_attention(const char* who, const Kv& kv, int32_t n) {
+  if (n < 1) return fail(MKA_ERR_INVALID_ARG, "%s: n must be >= 1", who);
+  if ((long long)kv.G * n > (1 << 20) || (long long)kv.a.B * n * kv.Hq > (1LL << 30))
+    return fail(MKA_ERR_UNSUPPORTED, "%s: too many query rows", who);
+  const long long units = (long long)kv.a.Hkv * (((long long)kv.G * n + 7) / 8), tiles = (kv.a.Lmax + 127) / 128;
+  if (units * tiles > 0x7fffffff || units * kv.a.B > 0x7fffffff)
+    return fail(MKA_ERR_UNSUPPORTED, "%s: max_positions times query rows too large", who);
+  return MKA_OK;
+}
+#define TRY(expr)                  \
+  do {                             \
+    const int t_ = (expr);         \
+    if (t_ != MKA_OK) return t_;   \
+  } while (0)
+
 }  // namespace
 
 extern "C" {
+
+int mka_kv8_append(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const void* k_new, const void* v_new,
+                   int64_t row_stride, int64_t batch_stride, int32_t n, const int32_t* pos, const int32_t* count,
+                   void* stream) {
+  Kv kv;
+  if (!cache) return fail(MKA_ERR_INVALID_ARG, "%s: cache is NULL", __func__);
+  TRY(check_kv8(__func__, cfg, cache, &kv));
+  TRY(check_rows(__func__, kv, row_stride, batch_stride, n));
+  NEED(k_new); NEED(v_new);
+  TRY(check_positions(__func__, pos, "pos", true));
+  TRY(check_positions(__func__, count, "count", false));
+  int* status = device_status();
+  if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
+  CUDA_TRY(kv8_append(kv.a, k_new, v_new, kv.bf16, row_stride, batch_stride, n, pos, count, status, (cudaStream_t)stream));
+  return MKA_OK;
+}
+
+int mka_kv8_read(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const int32_t* first, const int32_t* rows,
+                 int32_t n, void* k_out, void* v_out, int64_t row_stride, int64_t batch_stride, void* stream) {
+  Kv kv;
+  if (!cache) return fail(MKA_ERR_INVALID_ARG, "%s: cache is NULL", __func__);
+  TRY(check_kv8(__func__, cfg, cache, &kv));
+  TRY(check_rows(__func__, kv, row_stride, batch_stride, n));
+  NEED(k_out); NEED(v_out);
+  TRY(check_positions(__func__, first, "first", false));
+  TRY(check_positions(__func__, rows, "rows", false));
+  int* status = device_status();
+  if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
+  CUDA_TRY(kv8_read(kv.a, first, rows, n, k_out, v_out, kv.bf16, row_stride, batch_stride, status, (cudaStream_t)stream));
+  return MKA_OK;
+}
+
+size_t mka_kv8_attention_workspace_size(const mka_kv8_config* cfg, int32_t n, int32_t with_weights) {
+  Kv kv;
+  size_t a, b;
+  if (check_kv8(__func__, cfg, nullptr, &kv) != MKA_OK || check_kv8_attention(__func__, kv, n) != MKA_OK) return 0;
+  return kv8_attention_scratch(kv.a, kv.G, n, with_weights, &a, &b);
+}
+
+int mka_kv8_attention(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const void* q, int32_t n, const int32_t* lens,
+                      void* out, float* weights, void* ws, size_t ws_bytes, void* stream) {
+  Kv kv;
+  if (!cache) return fail(MKA_ERR_INVALID_ARG, "%s: cache is NULL", __func__);
+  TRY(check_kv8(__func__, cfg, cache, &kv));
+  TRY(check_kv8_attention(__func__, kv, n));
+  NEED(q); NEED(out); NEED(ws);
+  TRY(check_positions(__func__, lens, "lens", true));
+  if ((uintptr_t)weights & 3) return fail(MKA_ERR_INVALID_ARG, "%s: weights is not aligned", __func__);
+  size_t stats, scores;
+  const size_t need = kv8_attention_scratch(kv.a, kv.G, n, weights != nullptr, &stats, &scores);
+  if (ws_bytes < need) return fail(MKA_ERR_WORKSPACE, "%s: ws holds %zu bytes, needs %zu", __func__, ws_bytes, need);
+  if (!device_status()) return fail(MKA_ERR_CUDA, "no CUDA device");
+  Kv8Attn a = {};
+  a.c = kv.a;
+  a.q = q; a.out = out; a.lens = lens; a.n = n; a.G = kv.G; a.window = kv.window; a.sinks = kv.sinks;
+  a.sl2 = kv.scale * 1.4426950408889634f;
+  a.part = (float*)ws;
+  a.weights = weights;
+  a.stats = (float*)((char*)ws + stats);
+  a.scores = (float*)((char*)ws + scores);
+  CUDA_TRY(kv8_attention(a, kv.bf16, (cudaStream_t)stream));
+  return MKA_OK;
+}
+
+size_t mka_kv8_evict_workspace_size(const mka_kv8_config* cfg, int32_t keep) {
+  Kv kv;
+  if (check_kv8(__func__, cfg, nullptr, &kv) != MKA_OK || keep < 1) return 0;
+  return 256;
+}
+
+int mka_kv8_evict(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const int32_t* lens, const float* weights,
+                  int32_t keep, int32_t first, int32_t recent, const mka_kv8_config* dst_cfg, const mka_kv8_cache* dst,
+                  int32_t* dst_lens, float* dst_weights, int32_t* kept, void* ws, size_t ws_bytes, void* stream) {
+  Kv s, d;
+  if (!cache || !dst) return fail(MKA_ERR_INVALID_ARG, "%s: cache or dst is NULL", __func__);
+  TRY(check_kv8(__func__, cfg, cache, &s));
+  TRY(check_kv8(__func__, dst_cfg, dst, &d));
+  if (d.a.B != s.a.B || d.a.Hkv != s.a.Hkv || d.a.dh != s.a.dh)
+    return fail(MKA_ERR_INVALID_ARG, "%s: dst must have the batch, KV heads and head size of the cache", __func__);
+  if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
+    return fail(MKA_ERR_INVALID_ARG, "%s: keep must be >= 1 and first + recent within it", __func__);
+  if (keep > d.a.Lmax) return fail(MKA_ERR_INVALID_ARG, "%s: keep exceeds the new cache", __func__);
+  if (cache->k == dst->k || cache->v == dst->v || cache->k_scale == dst->k_scale || cache->v_scale == dst->v_scale ||
+      (const void*)weights == dst_weights || (const void*)lens == dst_lens)
+    return fail(MKA_ERR_INVALID_ARG, "%s: dst must be another cache", __func__);
+  TRY(check_positions(__func__, lens, "lens", true));
+  TRY(check_positions(__func__, dst_lens, "dst_lens", true));
+  TRY(check_positions(__func__, kept, "kept", true));
+  if (!weights || ((uintptr_t)weights & 3) || ((uintptr_t)dst_weights & 3))
+    return fail(MKA_ERR_INVALID_ARG, "%s: weights is NULL or misaligned", __func__);
+  NEED(ws);
+  if (ws_bytes < mka_kv8_evict_workspace_size(cfg, keep)) return fail(MKA_ERR_WORKSPACE, "%s: ws is too small", __func__);
+  if (!device_status()) return fail(MKA_ERR_CUDA, "no CUDA device");
+  CUDA_TRY(kv8_evict(s.a, lens, weights, keep, first, recent, d.a, dst_lens, dst_weights, kept, (cudaStream_t)stream));
+  return MKA_OK;
+}
 
 int mka_window_attention(const mka_attn_config* cfg, const mka_attn_strides* strides, const void* q, const void* k,
                          const void* v, const int32_t* lens, void* out, float* lse, void* stream) {

@@ -279,6 +279,34 @@ struct DecodeArgs {
 // attention units); float32: GEMV, token update, split-KV attention and merge as four launches.
 cudaError_t decode_step(const DecodeArgs& a, cudaStream_t s);
 
+// ---------------------------------------------------------------- 8-bit K/V cache (kv8.cu)
+struct Kv8Args {
+  void *k, *v;       // e4m3 codes [B][Hkv][Lmax][dh], 16-byte aligned
+  float *ks, *vs;    // scales [B][Hkv][nblk], powers of two
+  int B, Hkv, dh, Lmax, block, nblk;  // block: 16, 32, 64 or 128; nblk = ceil(Lmax / block)
+};
+// Rows of K and V (head g of row t of sequence b at b * batch_stride + t * row_stride + g * dh) to
+// positions pos[b].. of the cache, count[b] (null: n) of them; see mka_kv8_append.
+cudaError_t kv8_append(const Kv8Args& a, const void* kn, const void* vn, int is_bf16, long long row_stride,
+                       long long batch_stride, int n, const int* pos, const int* count, int* status, cudaStream_t s);
+cudaError_t kv8_read(const Kv8Args& a, const int* first, const int* rows, int n, void* k_out, void* v_out, int is_bf16,
+                     long long row_stride, long long batch_stride, int* status, cudaStream_t s);
+struct Kv8Attn {
+  Kv8Args c;
+  const void* q; void* out;  // [B][n][Hkv * G * dh], float32 or bf16
+  const int* lens;           // [B]
+  int n, G, window, sinks;
+  float sl2;                 // score scale * log2(e)
+  float* part;               // partial results
+  float* weights;            // [B][Hkv][Lmax], nullable: += each token's summed softmax weight
+  float* stats;              // [B][Hkv][G n][2] with weights: each row's maximum (log2) and sum
+  float* scores;             // [B][Hkv][Lmax][G n] with weights: raw scores (log2 units)
+};
+size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t* stats, size_t* scores);
+cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, cudaStream_t s);
+cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, int keep, int first, int recent,
+                      const Kv8Args& d, int* lens2, float* weights2, int* kept, cudaStream_t s);
+
 // Waits `limit_us` on an mbarrier nothing arrives at; *result = 1 if the wait (wrongly) completed.
 cudaError_t selftest_wait_timeout(int limit_us, int* status, int* result, cudaStream_t s);
 

@@ -1,0 +1,970 @@
+// K/V cache held in 8 bits: append (quantise), read, attention of new tokens, eviction.
+//
+// Layout: codes [B][Hkv][Lmax][dh] e4m3, one float32 scale per (sequence, KV head, block of tokens)
+// [B][Hkv][ceil(Lmax / block)]; a row's values are code * scale.  The scale of a block is the smallest
+// power of two with max |value| <= 448 * scale (448: the largest e4m3 value).  A power of two costs the
+// floating-point codes no precision, makes code * scale exact, and lets a block whose scale grows
+// re-round its older codes without a second rounding error (only codes that fall below the smallest
+// normal one change).
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kernels.h"
+#include "common.cuh"
+
+namespace mka {
+namespace kv8 {
+
+constexpr float kQuietNaN = __builtin_nanf("");
+
+// 2^x for x in [-126, 127].
+__device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+// The smallest x >= -120 with amax <= 448 * 2^x (amax finite, >= 0): amax = 1.f * 2^(E - 127) and
+// 448 = 1.75 * 2^8, so x = E - 135, one more when the fraction exceeds .75.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  return max(-120, (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0));
+}
+__device__ __forceinline__ int exp_of(float p2) { return (int)(__float_as_uint(p2) >> 23) - 127; }
+
+// Two values to e4m3 (a in the low byte): round to nearest even; NaN and infinities become NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  a = isfinite(a) ? a : kQuietNaN;
+  b = isfinite(b) ? b : kQuietNaN;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Two e4m3 codes (16 bits) to half2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t lo16) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)lo16));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f2(uint32_t lo16) {
+  const uint32_t h = e4m3x2_to_h2(lo16);
+  return __half22float2(*(const __half2*)&h);
+}
+
+// 16 consecutive values as float (p 16-byte aligned).
+template <typename T> __device__ __forceinline__ void load16(const T* p, float (&x)[16]);
+template <> __device__ __forceinline__ void load16<float>(const float* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = ((const float4*)p)[i];
+    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+  }
+}
+template <> __device__ __forceinline__ void load16<bf16>(const bf16* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = ((const uint4*)p)[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+      x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+}
+template <typename T> __device__ __forceinline__ void store16(T* p, const float (&x)[16]);
+template <> __device__ __forceinline__ void store16<float>(float* p, const float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ((float4*)p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+template <> __device__ __forceinline__ void store16<bf16>(bf16* p, const float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]);
+      w[k] = *(const uint32_t*)&h;
+    }
+    ((uint4*)p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// 16 codes times a factor.
+__device__ __forceinline__ void decode16(const uint4& c, float f, float (&x)[16]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 a = e4m3x2_to_f2(w[k]), b = e4m3x2_to_f2(w[k] >> 16);
+    x[4 * k] = a.x * f; x[4 * k + 1] = a.y * f; x[4 * k + 2] = b.x * f; x[4 * k + 3] = b.y * f;
+  }
+}
+__device__ __forceinline__ uint4 encode16(const float (&x)[16], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w[k] = to_e4m3x2(x[4 * k] * inv, x[4 * k + 1] * inv) | (to_e4m3x2(x[4 * k + 2] * inv, x[4 * k + 3] * inv) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// max |x| over the finite values.
+__device__ __forceinline__ float amax16(const float (&x)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, isfinite(x[i]) ? fabsf(x[i]) : 0.f);
+  return m;
+}
+
+// Maximum over a block of NT threads (every thread gets it).
+template <int NT>
+__device__ __forceinline__ float block_max(float v, float* s) {
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float m = s[0];
+#pragma unroll
+  for (int i = 1; i < NT / 32; ++i) m = fmaxf(m, s[i]);
+  return m;
+}
+
+// ============================================================================ append
+// One block of threads per (touched token block, K or V and head, sequence).  The new rows of the token
+// block stay in registers between the maximum and the codes, so each is read once.
+constexpr int AP_THREADS = 256;
+
+template <typename T, int DH, int CH>  // CH: 16-value chunks per thread, CH * 256 >= block * DH / 16
+__global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* kn, const T* vn, long long row_stride,
+                                                            long long batch_stride, int n, const int* pos,
+                                                            const int* count, int* status) {
+  __shared__ float red[AP_THREADS / 32];
+  constexpr int CPR = DH / 16;  // chunks per row
+  const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+  const int p = pos[b], c = count ? min(max(count[b], 0), n) : n;
+  if (p < 0 || (long long)p + c > a.Lmax) {  // the whole sequence is left as it was
+    if (threadIdx.x == 0) set_status(status, p < 0 ? kStatusBounds : kStatusCapacity);
+    return;
+  }
+  const int tb = p / a.block + blockIdx.x, t0 = tb * a.block;
+  const int lo = max(p, t0), hi = min(p + c, t0 + a.block);  // new rows of this token block
+  if (lo >= hi) return;
+  uint8_t* codes = (uint8_t*)(kv ? a.v : a.k) + ((size_t)b * a.Hkv + g) * a.Lmax * DH;
+  float* scale = (kv ? a.vs : a.ks) + ((size_t)b * a.Hkv + g) * a.nblk + tb;
+  const T* x = (kv ? vn : kn) + (size_t)b * batch_stride + (size_t)g * DH;
+  const int nch = (hi - lo) * CPR;
+  float v[CH][16], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int ch = i * AP_THREADS + threadIdx.x;
+    if (ch < nch) {
+      load16<T>(x + (size_t)(lo - p + ch / CPR) * row_stride + ch % CPR * 16, v[i]);
+      m = fmaxf(m, amax16(v[i]));
+    }
+  }
+  const float old = lo > t0 ? *scale : 0.f;  // the scale of the rows that the block already holds
+  m = block_max<AP_THREADS>(m, red);         // (also: every thread has read the old scale)
+  int e = scale_exp(m);
+  if (lo > t0) e = max(e, exp_of(old));
+  const float inv = pow2(-e);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int ch = i * AP_THREADS + threadIdx.x;
+    if (ch < nch) *(uint4*)(codes + (size_t)(lo + ch / CPR) * DH + ch % CPR * 16) = encode16(v[i], inv);
+  }
+  if (lo > t0 && e != exp_of(old)) {
+    const float f = pow2(max(-126, exp_of(old) - e));  // below 2^-126 every code rounds to 0 anyway
+    for (int ch = threadIdx.x; ch < (lo - t0) * CPR; ch += AP_THREADS) {
+      uint4* at = (uint4*)(codes + (size_t)(t0 + ch / CPR) * DH + ch % CPR * 16);
+      float y[16];
+      decode16(*at, f, y);
+      *at = encode16(y, 1.f);
+    }
+  }
+  if (threadIdx.x == 0) *scale = pow2(e);
+}
+
+// ============================================================================ read
+// Thread per 16 codes; rows [first[b], first[b] + rows[b]) of sequence b to rows 0.. of the outputs.
+template <typename T, int DH>
+__global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, const int* rows, int n, T* k_out,
+                                                   T* v_out, long long row_stride, long long batch_stride, int* status) {
+  constexpr int CPR = DH / 16;
+  const int b = blockIdx.z, kv = blockIdx.y;
+  const int f = first ? first[b] : 0, r = rows ? min(max(rows[b], 0), n) : n;
+  if (f < 0 || (long long)f + r > a.Lmax) {
+    if (threadIdx.x == 0) set_status(status, kStatusBounds);
+    return;
+  }
+  // (row, head, chunk), chunk fastest: a warp writes 32 chunks of consecutive output columns
+  const int at = blockIdx.x * 256 + threadIdx.x, per = a.Hkv * CPR;
+  const int row = at / per, g = at % per / CPR, ch = at % CPR;
+  if (row >= r) return;
+  const size_t hd = (size_t)b * a.Hkv + g;
+  const uint8_t* codes = (const uint8_t*)(kv ? a.v : a.k) + (hd * a.Lmax + f + row) * DH + ch * 16;
+  const float s = (kv ? a.vs : a.ks)[hd * a.nblk + (f + row) / a.block];
+  float x[16];
+  decode16(*(const uint4*)codes, s, x);
+  store16<T>((kv ? v_out : k_out) + (size_t)b * batch_stride + (size_t)row * row_stride + g * DH + ch * 16, x);
+}
+
+// ============================================================================ attention
+// A unit is (sequence b, KV head g, group of 8 NT query rows); a query row is (new token i, query head of
+// g), row r = i * G + head.  Everything is computed transposed: S^T = K Q^T with 16 cached tokens as the
+// rows of a m16n8k16 product and 8 query rows as its columns, O^T = V^T P^T with 16 channels as the rows.
+// With a handful of query rows per KV head this wastes half as much of the products as 16-row query
+// tiles would, and both cached operands then go from global memory straight into registers as 16-byte
+// pieces of a token's row: the contraction index of S^T (channels) may be permuted freely, and the
+// channel order of O^T too, so a lane's 16 consecutive bytes serve as its fragments (K: bytes 4w..4w+3
+// of its piece are k-step w; V: byte pairs of two tokens, joined by prmt).  No shared memory, no copies.
+// e4m3 to half is exact; q enters as half after a power-of-two scaling of its row (SPLIT, float32 q: as
+// high and low halves); P as half, relative to the row's running reference (SPLIT: high and low).
+//
+// Work: the 128-token tiles that a unit's rows see, over all units in order, are cut into equal ranges,
+// one per CTA, so ragged batches stay balanced; a unit that falls into several ranges leaves partial
+// results (slot = CTA + unit, which increases along the ranges and never repeats) for merge_kernel.
+constexpr int AT_THREADS = 128;
+constexpr int TILE = 128;      // tokens per CTA step, 32 per warp
+constexpr float LAZY = 8.f;    // log2: the reference moves when it is exceeded by more
+
+struct Tiles {  // the 128-token tiles of a unit: tile i at i < nsk ? i : lo + i - nsk
+  int len, lo, nsk, n;
+  __device__ __forceinline__ int tile(int i) const { return i < nsk ? i : lo + i - nsk; }
+};
+__device__ __forceinline__ Tiles unit_tiles(const Kv8Attn& a, int b) {
+  Tiles t;
+  t.len = min(max(a.lens[b], 0), a.c.Lmax);
+  const int p0 = max(t.len - a.n, 0);  // the first query that has a position
+  t.lo = a.window ? max(0, p0 - a.window + 1) / TILE : 0;
+  t.nsk = min((a.sinks + TILE - 1) / TILE, t.lo);
+  t.n = t.len > 0 ? t.nsk + (t.len - 1) / TILE - t.lo + 1 : 0;
+  return t;
+}
+// Tiles of sequences [b0, b1) per (head, row group), summed by one warp's lanes or a single thread.
+__device__ __forceinline__ long long warp_sum_ll(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *(const uint32_t*)&h;
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t u) { return __half22float2(*(const __half2*)&u); }
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int DH> struct Piece;  // a lane's piece of a V row: DH / 8 bytes
+template <> struct Piece<128> { uint32_t w[4]; };
+template <> struct Piece<64> { uint32_t w[2]; };
+template <int DH> __device__ __forceinline__ Piece<DH> load_piece(const uint8_t* p);
+template <> __device__ __forceinline__ Piece<128> load_piece<128>(const uint8_t* p) {
+  const uint4 v = __ldg((const uint4*)p);
+  return {{v.x, v.y, v.z, v.w}};
+}
+template <> __device__ __forceinline__ Piece<64> load_piece<64>(const uint8_t* p) {
+  const uint2 v = __ldg((const uint2*)p);
+  return {{v.x, v.y}};
+}
+
+// NT: groups of 8 query rows; SPLIT: float32 queries and outputs; WT: raw scores go to a.scores.
+template <typename T, int DH, int NT, bool WT>
+__global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(Kv8Attn a) {
+  constexpr bool SPLIT = sizeof(T) == 4;
+  constexpr int KW = DH / 16;      // 32-bit words of a K row per lane = k-steps of S^T
+  constexpr int MT = DH / 16;      // 16-channel tiles of O^T
+  constexpr int VW = DH / 32;      // 32-bit words of a V row per lane
+  constexpr int RT = 8 * NT;
+  __shared__ float sO[4][RT][DH + 4];
+  __shared__ float sStat[4][RT][3];  // ml, l, mu of each warp
+  __shared__ long long sScan[AT_THREADS / 32];
+  __shared__ int sStart[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, c4 = lane & 3;
+  const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg;  // units per sequence
+
+  // this CTA's range of tiles [w0, w1) and the sequence that w0 falls into
+  long long total;
+  {
+    const int per = (a.c.B + AT_THREADS - 1) / AT_THREADS, b0 = min(threadIdx.x * per, a.c.B), b1 = min(b0 + per, a.c.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += (long long)unit_tiles(a, b).n * upb;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sScan[warp] = inc;
+    __syncthreads();
+    long long before = inc - mine;
+    total = 0;
+    for (int i = 0; i < AT_THREADS / 32; ++i) {
+      if (i < warp) before += sScan[i];
+      total += sScan[i];
+    }
+    const long long share = (total + gridDim.x - 1) / gridDim.x, w0 = share * blockIdx.x;
+    if (w0 >= before && w0 < before + mine) {  // one thread at most
+      long long left = w0 - before;
+      int b = b0;
+      for (;; ++b) {
+        const long long t = (long long)unit_tiles(a, b).n * upb;
+        if (left < t) break;
+        left -= t;
+      }
+      sStart[0] = b;
+      sStart[1] = (int)left;  // tiles of sequence b before w0
+    }
+    __syncthreads();
+  }
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long w0 = share * blockIdx.x, w1 = min(total, w0 + share);
+  if (w0 >= w1) return;
+  int todo = (int)(w1 - w0), b = sStart[0];
+  Tiles ts = unit_tiles(a, b);
+  int u = sStart[1] / ts.n, first = sStart[1] % ts.n;  // unit within the sequence, its first tile here
+
+  while (todo > 0) {
+    const int cnt = min(todo, ts.n - first);
+    const int g = u / nrg, rg = u % nrg;
+    const size_t hd = (size_t)b * a.c.Hkv + g;
+    const uint8_t* kc = (const uint8_t*)a.c.k + hd * a.c.Lmax * DH;
+    const uint8_t* vc = (const uint8_t*)a.c.v + hd * a.c.Lmax * DH;
+    const float* ksc = a.c.ks + hd * a.c.nblk;
+    const float* vsc = a.c.vs + hd * a.c.nblk;
+
+    // Q^T fragments of row g8 of each group: k-step w holds the channels of bytes 4w..4w+3 of the
+    // lane's K pieces; the row is scaled by a power of two to a maximum in [2^7, 2^8)
+    uint32_t qf[NT][KW][2], ql[SPLIT ? NT : 1][SPLIT ? KW : 1][2];
+    float rf[NT][2];       // score factor of the rows of this lane's accumulators (2 c4 and 2 c4 + 1)
+    int qpos[NT][2];       // their positions; -1: not a row
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = rg * RT + t * 8 + g8;
+      const bool in = r < R;
+      const T* qr = (const T*)a.q + ((size_t)b * a.n + (in ? r / a.G : 0)) * (size_t)(a.c.Hkv * a.G * DH) +
+                    (size_t)(g * a.G + (in ? r % a.G : 0)) * DH;
+      float x[KW][4], m = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const int d = (w >> 2) * 64 + c4 * 16 + (w & 3) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[w][i] = in ? to_f<T>(qr[d + i]) : 0.f;
+          m = fmaxf(m, fabsf(x[w][i]));
+        }
+      }
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = min(max((int)(__float_as_uint(m) >> 23) - 127 - 7, -119), 119);
+      const float down = pow2(-e);
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float y0 = x[w][2 * i] * down, y1 = x[w][2 * i + 1] * down;
+          qf[t][w][i] = pack_h2(y0, y1);
+          if constexpr (SPLIT) {
+            const float2 h = unpack_h2(qf[t][w][i]);
+            ql[t][w][i] = pack_h2(y0 - h.x, y1 - h.y);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rf[t][i] = pow2(__shfl_sync(0xffffffffu, e, (2 * c4 + i) * 4)) * a.sl2;
+        const int rr = rg * RT + t * 8 + 2 * c4 + i;
+        qpos[t][i] = rr < R ? ts.len - a.n + rr / a.G : -1;
+      }
+    }
+    const int p_lo = ts.len - a.n + rg * RT / a.G, p_hi = ts.len - a.n + (min(R, (rg + 1) * RT) - 1) / a.G;
+
+    float o[MT][NT][4], l[NT][2], ml[NT][2], mu[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[t][i] = 0.f;
+        ml[t][i] = mu[t][i] = -INFINITY;
+      }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[m][t][i] = 0.f;
+
+    uint4 kr[2][2][DH / 64];  // [16-token half][token g8 or g8 + 8][64-byte half of the row]
+    Piece<DH> vr[2][4];       // [16-token half][token 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9]
+    float ks[2], vs[2];
+    auto load_k = [&](int j0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ks[h] = __ldg(ksc + min((j0 + 16 * h) / a.c.block, a.c.nblk - 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* p = kc + (size_t)min(j0 + 16 * h + 8 * i + g8, a.c.Lmax - 1) * DH + c4 * 16;
+#pragma unroll
+          for (int q = 0; q < DH / 64; ++q) kr[h][i][q] = __ldg((const uint4*)(p + q * 64));
+        }
+      }
+    };
+    auto load_v = [&](int j0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        vs[h] = __ldg(vsc + min((j0 + 16 * h) / a.c.block, a.c.nblk - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vr[h][i] = load_piece<DH>(vc + (size_t)min(j0 + 16 * h + 2 * c4 + (i & 1) + 8 * (i >> 1), a.c.Lmax - 1) * DH +
+                                    g8 * (DH / 8));
+      }
+    };
+    auto sees = [&](int j, int p) { return j <= p && (!a.window || j > p - a.window || j < a.sinks); };
+
+    load_k(ts.tile(first) * TILE + warp * 32);
+    load_v(ts.tile(first) * TILE + warp * 32);
+    for (int it = 0; it < cnt; ++it) {
+      const int j0 = ts.tile(first + it) * TILE + warp * 32;
+      const int jn = it + 1 < cnt ? ts.tile(first + it + 1) * TILE + warp * 32 : -1;
+      // S^T of 32 tokens
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[h][t][i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const uint4 &x0 = kr[h][0][w >> 2], &x1 = kr[h][1][w >> 2];
+          const uint32_t y0 = (w & 3) == 0 ? x0.x : (w & 3) == 1 ? x0.y : (w & 3) == 2 ? x0.z : x0.w;
+          const uint32_t y1 = (w & 3) == 0 ? x1.x : (w & 3) == 1 ? x1.y : (w & 3) == 2 ? x1.z : x1.w;
+          const uint32_t a0 = e4m3x2_to_h2(y0), a1 = e4m3x2_to_h2(y1), a2 = e4m3x2_to_h2(y0 >> 16),
+                         a3 = e4m3x2_to_h2(y1 >> 16);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(s[h][t], a0, a1, a2, a3, qf[t][w][0], qf[t][w][1]);
+            if constexpr (SPLIT) mma16816(s[h][t], a0, a1, a2, a3, ql[t][w][0], ql[t][w][1]);
+          }
+        }
+      }
+      const float kf[2] = {ks[0], ks[1]};
+      if (jn >= 0) load_k(jn);
+
+      // scores in log2 units; hidden ones -inf
+      const bool edge = j0 + 31 > p_lo || (a.window && j0 <= p_hi - a.window && j0 + 31 >= a.sinks);  // warp-uniform
+      const float ev[2] = {(float)exp_of(vs[0]), (float)exp_of(vs[1])};
+      bool over = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // token j0 + 16 h + g8 + 8 (i / 2), row 2 c4 + i % 2
+            float x = s[h][t][i] * (kf[h] * rf[t][i & 1]);
+            if (edge && !sees(j0 + 16 * h + g8 + 8 * (i >> 1), qpos[t][i & 1])) x = -INFINITY;
+            s[h][t][i] = x;
+            over |= x > ml[t][i & 1] + LAZY || x + ev[h] > mu[t][i & 1] + LAZY;
+          }
+      if constexpr (WT) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 16 * h + g8 + 8 * (i >> 1), r = rg * RT + t * 8 + 2 * c4 + (i & 1);
+              if (j < ts.len && r < R) a.scores[(hd * a.c.Lmax + j) * R + r] = s[h][t][i];
+            }
+      }
+      if (__any_sync(0xffffffffu, over)) {  // move the references to the tile's maxima
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float z = fmaxf(s[h][t][i], s[h][t][i + 2]);
+              x = fmaxf(x, z);
+              y = fmaxf(y, z + ev[h]);
+            }
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, k));
+            }
+            if (x > ml[t][i]) {
+              l[t][i] *= ex2f(ml[t][i] - x);
+              ml[t][i] = x;
+            }
+            if (y > mu[t][i]) {
+              const float f = ex2f(mu[t][i] - y);
+              mu[t][i] = y;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                o[m][t][i] *= f;
+                o[m][t][i + 2] *= f;
+              }
+            }
+          }
+      }
+      // P^T: the fragments of S^T transposed into those of a B operand
+      uint32_t pf[2][NT][2], pl[2][SPLIT ? NT : 1][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float y[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float x = s[h][t][2 * i + k];
+              const bool hid = edge && x == -INFINITY;
+              y[k] = hid ? 0.f : ex2f(x + ev[h] - mu[t][k]);
+              l[t][k] += hid ? 0.f : ex2f(x - ml[t][k]);
+            }
+            const uint32_t hi = pack_h2(y[0], y[1]);
+            pf[h][t][i] = transpose8x8(hi);
+            if constexpr (SPLIT) {
+              const float2 f = unpack_h2(hi);
+              pl[h][t][i] = transpose8x8(pack_h2(y[0] - f.x, y[1] - f.y));
+            }
+          }
+      if (edge) {
+        // a hidden token's P is 0, but 0 * NaN is not: its NaN codes are cleared, and the rows that do
+        // see such a token get their NaN directly
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t nan[4];  // bit d: channel d of this lane's piece of token slot i is NaN
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            nan[i] = 0;
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (((vr[h][i].w[w] >> (8 * k)) & 0x7f) == 0x7f) {
+                  nan[i] |= 1u << (4 * w + k);
+                  vr[h][i].w[w] &= ~(0xffu << (8 * k));
+                }
+            any |= nan[i];
+          }
+          if (__any_sync(0xffffffffu, any != 0)) {
+            for (int src = 0; src < 4; ++src)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = __shfl_sync(0xffffffffu, nan[i], (lane & ~3) | src);
+                const int j = j0 + 16 * h + 2 * src + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                  for (int k = 0; k < 2; ++k)
+                    if (bits && sees(j, qpos[t][k]))
+#pragma unroll
+                      for (int m = 0; m < MT; ++m) {
+                        if ((bits >> (2 * m)) & 1) o[m][t][k] = kQuietNaN;
+                        if ((bits >> (2 * m + 1)) & 1) o[m][t][k + 2] = kQuietNaN;
+                      }
+              }
+          }
+        }
+      }
+      // O^T += V^T P^T; channel tile m holds the channels 2m and 2m + 1 of each lane's piece
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t sel = (m & 1) ? 0x7362u : 0x5140u;
+          const uint32_t x = __byte_perm(vr[h][0].w[m >> 1], vr[h][1].w[m >> 1], sel);
+          const uint32_t y = __byte_perm(vr[h][2].w[m >> 1], vr[h][3].w[m >> 1], sel);
+          const uint32_t a0 = e4m3x2_to_h2(x), a1 = e4m3x2_to_h2(x >> 16), a2 = e4m3x2_to_h2(y), a3 = e4m3x2_to_h2(y >> 16);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(o[m][t], a0, a1, a2, a3, pf[h][t][0], pf[h][t][1]);
+            if constexpr (SPLIT) mma16816(o[m][t], a0, a1, a2, a3, pl[h][t][0], pl[h][t][1]);
+          }
+        }
+      if (jn >= 0) load_v(jn);
+    }
+
+    // join the four warps
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = l[t][i];
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+        const int r = t * 8 + 2 * c4 + i;
+        if (g8 == 0) {
+          sStat[warp][r][0] = ml[t][i];
+          sStat[warp][r][1] = x;
+          sStat[warp][r][2] = mu[t][i];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          *(float2*)&sO[warp][r][g8 * (DH / 8) + 2 * m] = make_float2(o[m][t][i], o[m][t][i + 2]);
+      }
+    __syncthreads();
+    const bool whole = first == 0 && cnt == ts.n;
+    const size_t slot = (size_t)blockIdx.x + (size_t)b * upb + u;
+    for (int at = threadIdx.x; at < RT * (DH / 4); at += AT_THREADS) {
+      const int r = at / (DH / 4), d = at % (DH / 4) * 4, row = rg * RT + r;
+      if (row >= R) continue;
+      float L = -INFINITY, U = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        L = fmaxf(L, sStat[w][r][0]);
+        U = fmaxf(U, sStat[w][r][2]);
+      }
+      float sum = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float fl = sStat[w][r][0] == -INFINITY ? 0.f : ex2f(sStat[w][r][0] - L);
+        const float fu = sStat[w][r][2] == -INFINITY ? 0.f : ex2f(sStat[w][r][2] - U);
+        sum += sStat[w][r][1] * (sStat[w][r][1] == 0.f ? 1.f : fl);
+        const float4 y = *(const float4*)&sO[w][r][d];
+        // (a warp that saw nothing holds zeros, or the NaN of a NaN score: added as it is)
+        const float f = sStat[w][r][2] == -INFINITY ? 1.f : fu;
+        x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
+      }
+      if (whole) {
+        const float f = sum == 0.f ? 0.f : ex2f(U - L) / sum;  // a row that sees nothing is 0
+        T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) +
+                 (size_t)(g * a.G + row % a.G) * DH + d;
+        out[0] = from_f<T>(x.x * f); out[1] = from_f<T>(x.y * f); out[2] = from_f<T>(x.z * f); out[3] = from_f<T>(x.w * f);
+        if (WT && d == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
+      } else {
+        float* rec = a.part + (slot * RT + r) * (DH + 4);
+        *(float4*)(rec + 4 + d) = x;
+        if (d == 0) *(float4*)rec = make_float4(L, sum, U, 0.f);
+      }
+    }
+    __syncthreads();
+    todo -= cnt;
+    first = 0;
+    if (todo > 0 && ++u == upb) {
+      u = 0;
+      do ts = unit_tiles(a, ++b);
+      while (ts.n == 0);
+    }
+  }
+}
+
+// Joins the partial results of one query row of one unit; a unit without tiles gives 0.  One CTA of DH
+// threads (a channel each) per (unit, row).
+template <typename T, int DH, bool WT>
+__global__ void __launch_bounds__(DH) merge_kernel(Kv8Attn a, int RT, int grid) {
+  __shared__ long long s[DH / 32][2];
+  const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg;
+  const int row = blockIdx.x, g = blockIdx.y, b = blockIdx.z, rg = row / RT, r = row % RT, u = g * nrg + rg;
+  const Tiles ts = unit_tiles(a, b);
+  long long before = 0, total = 0;
+  for (int i = threadIdx.x; i < a.c.B; i += DH) {
+    const long long t = (long long)unit_tiles(a, i).n * upb;
+    total += t;
+    if (i < b) before += t;
+  }
+  before = warp_sum_ll(before);
+  total = warp_sum_ll(total);
+  if ((threadIdx.x & 31) == 0) {
+    s[threadIdx.x >> 5][0] = before;
+    s[threadIdx.x >> 5][1] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+  for (int i = 0; i < DH / 32; ++i) {
+    before += s[i][0];
+    total += s[i][1];
+  }
+  const size_t hd = (size_t)b * a.c.Hkv + g;
+  T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) + (size_t)(g * a.G + row % a.G) * DH +
+           threadIdx.x;
+  if (ts.n == 0) {
+    *out = from_f<T>(0.f);
+    return;
+  }
+  const long long share = (total + grid - 1) / grid, start = before + (long long)u * ts.n, end = start + ts.n - 1;
+  const int c0 = (int)(start / share), c1 = (int)(end / share);
+  if (c0 == c1) return;  // written whole by its CTA
+  const size_t slot0 = (size_t)b * upb + u;
+  float L = -INFINITY, U = -INFINITY, sum = 0.f, x = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const float* rec = a.part + ((slot0 + c) * RT + r) * (DH + 4);
+    L = fmaxf(L, rec[0]);
+    U = fmaxf(U, rec[2]);
+  }
+  for (int c = c0; c <= c1; ++c) {
+    const float* rec = a.part + ((slot0 + c) * RT + r) * (DH + 4);
+    const float l = rec[1];
+    sum += rec[0] == -INFINITY ? l : l * ex2f(rec[0] - L);
+    const float y = rec[4 + threadIdx.x];
+    x += rec[2] == -INFINITY ? y : y * ex2f(rec[2] - U);
+  }
+  *out = from_f<T>(sum == 0.f ? 0.f : x * (ex2f(U - L) / sum));
+  if (WT && threadIdx.x == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
+}
+
+// weights[b][g][j] += sum over the query rows of KV head g of their softmax weight of token j, from the
+// raw scores (log2 units) and each row's maximum and sum.  Thread per token of the unit's tiles.
+__global__ void __launch_bounds__(128) weights_kernel(Kv8Attn a) {
+  const int b = blockIdx.z, g = blockIdx.y;
+  const Tiles ts = unit_tiles(a, b);
+  if (blockIdx.x >= ts.n) return;
+  const int j = ts.tile(blockIdx.x) * TILE + threadIdx.x, R = a.G * a.n;
+  if (j >= ts.len) return;
+  const size_t hd = (size_t)b * a.c.Hkv + g;
+  const float* s = a.scores + (hd * a.c.Lmax + j) * R;
+  const float2* st = (const float2*)a.stats + hd * R;
+  float w = 0.f;
+  for (int r = 0; r < R; ++r) {
+    const float2 x = st[r];
+    const float y = s[r];
+    if (y != -INFINITY) w += ex2f(y - x.x) / x.y;
+  }
+  a.weights[hd * a.c.Lmax + j] += w;
+}
+
+// ============================================================================ eviction
+// Order of the weights as unsigned integers: larger float, larger key (NaN above infinity).
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);  // -0 and 0 are equal
+  return isnan(w) ? 0xffffffffu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// One CTA per (sequence, KV head): four passes of 8 bits find the key of the last kept token among the
+// middle ones [first, len - recent), then one pass in index order writes the kept tokens: every forced
+// one, every key above the found one, and the first `ties` with exactly that key.
+constexpr int SEL_THREADS = 1024;
+__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weights, int Lmax, int Hkv, const int* lens,
+                                                             int keep, int first, int recent, int* kept, int* lens2,
+                                                             float* weights2, int L2max) {
+  __shared__ int hist[256];
+  __shared__ int sh[4];
+  __shared__ int wsum[2][SEL_THREADS / 32];
+  const int hd = blockIdx.x, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int len = min(max(lens[b], 0), Lmax);
+  const float* w = weights + (size_t)hd * Lmax;
+  int* out = kept + (size_t)hd * keep;
+  float* w2 = weights2 ? weights2 + (size_t)hd * L2max : nullptr;
+  if (threadIdx.x == 0 && hd % Hkv == 0) lens2[b] = min(len, keep);
+  if (len <= keep) {  // all of a short sequence
+    for (int i = threadIdx.x; i < keep; i += SEL_THREADS) {
+      out[i] = i < len ? i : -1;
+      if (w2 && i < len) w2[i] = w[i];
+    }
+    return;
+  }
+  const int m0 = first, m1 = len - recent;
+  int need = keep - first - recent;  // of the middle tokens; fewer than there are
+  uint32_t prefix = 0;
+  for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
+    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = m0 + threadIdx.x; i < m1; i += SEL_THREADS) {
+      const uint32_t k = weight_key(w[i]);
+      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {  // largest bins first
+      int d = 255, left = need;
+      while (hist[d] < left) left -= hist[d--];
+      sh[0] = d;
+      sh[1] = left;
+    }
+    __syncthreads();
+    prefix = prefix << 8 | (uint32_t)sh[0];
+    need = sh[1];
+    __syncthreads();
+  }
+  // prefix: the key of the last kept middle token; need: how many with exactly that key
+  const bool none = keep == first + recent;
+  int nkept = 0, nties = 0;
+  for (int base = 0; base < len; base += SEL_THREADS) {
+    const int i = base + threadIdx.x;
+    const bool in = i < len, mid = in && i >= m0 && i < m1;
+    const uint32_t k = mid ? weight_key(w[i]) : 0;
+    const bool tie = mid && !none && k == prefix;
+    const unsigned tb = __ballot_sync(0xffffffffu, tie);
+    if (lane == 0) wsum[0][warp] = __popc(tb);
+    __syncthreads();
+    int t = nties + __popc(tb & ((1u << lane) - 1)), tall = nties;
+    for (int x = 0; x < SEL_THREADS / 32; ++x) {
+      if (x < warp) t += wsum[0][x];
+      tall += wsum[0][x];
+    }
+    const bool take = in && (!mid || (!none && k > prefix) || (tie && t < need));
+    const unsigned kb = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) wsum[1][warp] = __popc(kb);
+    __syncthreads();
+    int at = nkept + __popc(kb & ((1u << lane) - 1)), kall = nkept;
+    for (int x = 0; x < SEL_THREADS / 32; ++x) {
+      if (x < warp) at += wsum[1][x];
+      kall += wsum[1][x];
+    }
+    if (take && at < keep) {
+      out[at] = i;
+      if (w2) w2[at] = w[i];
+    }
+    nkept = kall;
+    nties = tall;
+    __syncthreads();
+  }
+}
+
+// Kept rows into the new cache, a token block at a time: one CTA per (block, K or V and head, sequence).
+template <int DH, int CH>
+__global__ void __launch_bounds__(256) compact_kernel(Kv8Args a, Kv8Args d, const int* kept, int keep, const int* lens2) {
+  __shared__ float red[8];
+  constexpr int CPR = DH / 16;
+  const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+  const int t0 = blockIdx.x * d.block, rows = min(d.block, lens2[b] - t0);
+  if (rows <= 0) return;
+  const size_t hd = (size_t)b * a.Hkv + g;
+  const uint8_t* src = (const uint8_t*)(kv ? a.v : a.k) + hd * a.Lmax * DH;
+  const float* ss = (kv ? a.vs : a.ks) + hd * a.nblk;
+  uint8_t* dst = (uint8_t*)(kv ? d.v : d.k) + (hd * d.Lmax + t0) * DH;
+  float v[CH][16], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int ch = i * 256 + threadIdx.x;
+    if (ch < rows * CPR) {
+      const int j = kept[hd * keep + t0 + ch / CPR];
+      decode16(*(const uint4*)(src + (size_t)j * DH + ch % CPR * 16), ss[j / a.block], v[i]);
+      m = fmaxf(m, amax16(v[i]));
+    }
+  }
+  m = block_max<256>(m, red);
+  const int e = scale_exp(m);
+  const float inv = pow2(-e);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int ch = i * 256 + threadIdx.x;
+    if (ch < rows * CPR) *(uint4*)(dst + (size_t)(ch / CPR) * DH + ch % CPR * 16) = encode16(v[i], inv);
+  }
+  if (threadIdx.x == 0) (kv ? d.vs : d.ks)[hd * d.nblk + blockIdx.x] = pow2(e);
+}
+
+// Calls f(integral_constant) with the 16-value chunks per thread of a token block of 256 threads.
+template <typename F>
+cudaError_t with_chunks(int block, int dh, F f) {
+  const int ch = (block * dh / 16 + 255) / 256;
+  if (ch <= 1) return f(std::integral_constant<int, 1>());
+  if (ch <= 2) return f(std::integral_constant<int, 2>());
+  return f(std::integral_constant<int, 4>());
+}
+
+}  // namespace kv8
+
+cudaError_t kv8_append(const Kv8Args& a, const void* kn, const void* vn, int is_bf16, long long row_stride,
+                       long long batch_stride, int n, const int* pos, const int* count, int* status, cudaStream_t s) {
+  const dim3 grid((n + a.block - 1 + a.block - 1) / a.block, 2 * a.Hkv, a.B);
+  auto run = [&](auto dh) {
+    constexpr int DH = decltype(dh)::value;
+    return kv8::with_chunks(a.block, DH, [&](auto ch) {
+      constexpr int CH = decltype(ch)::value;
+      if (is_bf16)
+        kv8::append_kernel<bf16, DH, CH><<<grid, kv8::AP_THREADS, 0, s>>>(a, (const bf16*)kn, (const bf16*)vn, row_stride,
+                                                                         batch_stride, n, pos, count, status);
+      else
+        kv8::append_kernel<float, DH, CH><<<grid, kv8::AP_THREADS, 0, s>>>(a, (const float*)kn, (const float*)vn,
+                                                                          row_stride, batch_stride, n, pos, count, status);
+      return cudaGetLastError();
+    });
+  };
+  return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
+}
+
+cudaError_t kv8_read(const Kv8Args& a, const int* first, const int* rows, int n, void* k_out, void* v_out, int is_bf16,
+                     long long row_stride, long long batch_stride, int* status, cudaStream_t s) {
+  const long long chunks = (long long)n * a.Hkv * (a.dh / 16);
+  const dim3 grid((unsigned)((chunks + 255) / 256), 2, a.B);
+  auto run = [&](auto dh) {
+    constexpr int DH = decltype(dh)::value;
+    if (is_bf16)
+      kv8::read_kernel<bf16, DH><<<grid, 256, 0, s>>>(a, first, rows, n, (bf16*)k_out, (bf16*)v_out, row_stride,
+                                                      batch_stride, status);
+    else
+      kv8::read_kernel<float, DH><<<grid, 256, 0, s>>>(a, first, rows, n, (float*)k_out, (float*)v_out, row_stride,
+                                                       batch_stride, status);
+    return cudaGetLastError();
+  };
+  return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
+}
+
+// Groups of 8 query rows per unit: a second group shares the cache's bytes and conversions, but takes
+// registers that otherwise hold a third CTA per SM.
+static int kv8_groups(int R) { return R <= 8 ? 1 : 2; }
+static int kv8_grid(int R) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms * (kv8_groups(R) == 1 ? 3 : 2);
+}
+
+size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t* stats, size_t* scores) {
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t R = (size_t)G * n, RT = 8 * kv8_groups((int)R), nrg = (R + RT - 1) / RT;
+  size_t o = al((kv8_grid((int)R) + (size_t)c.B * c.Hkv * nrg) * RT * (c.dh + 4) * 4);
+  *stats = o;
+  if (weights) o += al((size_t)c.B * c.Hkv * R * 8);
+  *scores = o;
+  if (weights) o += al((size_t)c.B * c.Hkv * c.Lmax * R * 4);
+  return o;
+}
+
+cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, cudaStream_t s) {
+  const int R = a.G * a.n, nt = kv8_groups(R), grid = kv8_grid(R);
+  auto run = [&](auto type, auto dh, auto nts, auto wt) {
+    using T = decltype(type);
+    constexpr int DH = decltype(dh)::value, NT = decltype(nts)::value;
+    constexpr bool WT = decltype(wt)::value;
+    kv8::attention_kernel<T, DH, NT, WT><<<grid, kv8::AT_THREADS, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    kv8::merge_kernel<T, DH, WT><<<dim3(R, a.c.Hkv, a.c.B), DH, 0, s>>>(a, 8 * NT, grid);
+    if ((e = cudaGetLastError()) != cudaSuccess || !WT) return e;
+    kv8::weights_kernel<<<dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, 0, s>>>(a);
+    return cudaGetLastError();
+  };
+  auto with_wt = [&](auto type, auto dh, auto nts) {
+    return a.weights ? run(type, dh, nts, std::true_type()) : run(type, dh, nts, std::false_type());
+  };
+  auto with_nt = [&](auto type, auto dh) {
+    return nt == 1 ? with_wt(type, dh, std::integral_constant<int, 1>())
+                   : with_wt(type, dh, std::integral_constant<int, 2>());
+  };
+  auto with_dh = [&](auto type) {
+    return a.c.dh == 128 ? with_nt(type, std::integral_constant<int, 128>())
+                         : with_nt(type, std::integral_constant<int, 64>());
+  };
+  return is_bf16 ? with_dh(bf16()) : with_dh(float());
+}
+
+cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, int keep, int first, int recent,
+                      const Kv8Args& d, int* lens2, float* weights2, int* kept, cudaStream_t s) {
+  kv8::select_kernel<<<a.B * a.Hkv, kv8::SEL_THREADS, 0, s>>>(weights, a.Lmax, a.Hkv, lens, keep, first, recent, kept, lens2,
+                                                             weights2, d.Lmax);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid((keep + d.block - 1) / d.block, 2 * a.Hkv, a.B);
+  auto run = [&](auto dh) {
+    constexpr int DH = decltype(dh)::value;
+    return kv8::with_chunks(d.block, DH, [&](auto ch) {
+      kv8::compact_kernel<DH, decltype(ch)::value><<<grid, 256, 0, s>>>(a, d, kept, keep, lens2);
+      return cudaGetLastError();
+    });
+  };
+  return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
+}
+
+}  // namespace mka
