@@ -271,13 +271,14 @@ def _dtype(t: torch.Tensor, want: torch.dtype, name: str) -> None:
 def _call_stream(tensors, stream):
     """The stream pointer of a call on `tensors`: they must live on the current device, and a stream
     other than the current one is recorded on them."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"every tensor of the call must live on the current CUDA device ({dev})")
+    current = torch._C._cuda_getCurrentRawStream(dev)  # (a Stream object per call would cost microseconds)
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        return current
+    if stream.cuda_stream != current:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)

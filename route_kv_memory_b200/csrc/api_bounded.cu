@@ -99,7 +99,7 @@ int check_kv8(const char* who, const mka_kv8_config* c, const mka_kv8_cache* cac
   if (c->window < 0 || c->sinks < 0) return fail(MKA_ERR_INVALID_ARG, "%s: window and sinks must be >= 0", who);
   if (c->batch > 65535 || c->n_kv_heads > 32767 || c->max_positions > (1 << 28) ||
       (long long)c->n_q_heads * c->d_head > (1LL << 24) || (long long)c->batch * c->n_kv_heads > (1 << 20) ||
-      (long long)c->batch * c->n_kv_heads * c->max_positions > (1LL << 36))
+      (long long)c->batch * c->n_kv_heads * c->max_positions > 0x7fffffffLL - 128)
     return fail(MKA_ERR_UNSUPPORTED, "%s: batch, heads or max_positions too large", who);
   o->a = {nullptr, nullptr, nullptr, nullptr, c->batch, c->n_kv_heads, c->d_head, c->max_positions, c->block,
           (c->max_positions + c->block - 1) / c->block};
@@ -199,7 +199,8 @@ int mka_kv8_attention(const mka_kv8_config* cfg, const mka_kv8_cache* cache, con
   size_t stats, scores;
   const size_t need = kv8_attention_scratch(kv.a, kv.G, n, weights != nullptr, &stats, &scores);
   if (ws_bytes < need) return fail(MKA_ERR_WORKSPACE, "%s: ws holds %zu bytes, needs %zu", __func__, ws_bytes, need);
-  if (!device_status()) return fail(MKA_ERR_CUDA, "no CUDA device");
+  int* status = device_status();
+  if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
   Kv8Attn a = {};
   a.c = kv.a;
   a.q = q; a.out = out; a.lens = lens; a.n = n; a.G = kv.G; a.window = kv.window; a.sinks = kv.sinks;
@@ -208,7 +209,7 @@ int mka_kv8_attention(const mka_kv8_config* cfg, const mka_kv8_cache* cache, con
   a.weights = weights;
   a.stats = (float*)((char*)ws + stats);
   a.scores = (float*)((char*)ws + scores);
-  CUDA_TRY(kv8_attention(a, kv.bf16, (cudaStream_t)stream));
+  CUDA_TRY(kv8_attention(a, kv.bf16, status, (cudaStream_t)stream));
   return MKA_OK;
 }
 

@@ -303,7 +303,7 @@ struct Kv8Attn {
   float* scores;             // [B][Hkv][Lmax][G n] with weights: raw scores (log2 units)
 };
 size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t* stats, size_t* scores);
-cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, cudaStream_t s);
+cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream_t s);
 cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, int keep, int first, int recent,
                       const Kv8Args& d, int* lens2, float* weights2, int* kept, cudaStream_t s);
 

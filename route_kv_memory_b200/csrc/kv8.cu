@@ -11,9 +11,12 @@
 #include <type_traits>
 
 #include "kernels.h"
-#include "common.cuh"
+#include "sm100.cuh"
 
 namespace mka {
+
+cudaError_t make_tmap_u8(CUtensorMap* map, const void* base, long long rows, int cols, int box_rows);
+
 namespace kv8 {
 
 constexpr float kQuietNaN = __builtin_nanf("");
@@ -203,20 +206,25 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
 // ============================================================================ attention
 // A unit is (sequence b, KV head g, group of 8 NT query rows); a query row is (new token i, query head of
 // g), row r = i * G + head.  Everything is computed transposed: S^T = K Q^T with 16 cached tokens as the
-// rows of a m16n8k16 product and 8 query rows as its columns, O^T = V^T P^T with 16 channels as the rows.
-// With a handful of query rows per KV head this wastes half as much of the products as 16-row query
-// tiles would, and both cached operands then go from global memory straight into registers as 16-byte
-// pieces of a token's row: the contraction index of S^T (channels) may be permuted freely, and the
-// channel order of O^T too, so a lane's 16 consecutive bytes serve as its fragments (K: bytes 4w..4w+3
-// of its piece are k-step w; V: byte pairs of two tokens, joined by prmt).  No shared memory, no copies.
+// rows of a m16n8k16 product and 8 query rows as its columns, O^T = V^T P^T with 16 channels as the rows:
+// with a handful of query rows per KV head this wastes half as much of the products as 16-row query
+// tiles would.  A contraction index may be permuted freely, and the channel order of O^T too, so the 16
+// consecutive bytes that a lane loads of a token's row serve as its fragments without any transposition
+// (K: bytes 4w..4w+3 of its pieces are k-step w; V: byte pairs of two tokens, joined by prmt).
 // e4m3 to half is exact; q enters as half after a power-of-two scaling of its row (SPLIT, float32 q: as
 // high and low halves); P as half, relative to the row's running reference (SPLIT: high and low).
+//
+// Every warp streams its own 32 tokens of each 128-token tile through its own two stages of shared
+// memory, filled by TMA (K and V, 32 rows each) with the 128-byte (d_head 64: 64-byte) swizzle: no
+// barrier across warps in the loop, 16 KB per warp in flight.  The token order inside 16 rows
+// (slot_token) is chosen so that both kinds of fragment loads are free of bank conflicts.
 //
 // Work: the 128-token tiles that a unit's rows see, over all units in order, are cut into equal ranges,
 // one per CTA, so ragged batches stay balanced; a unit that falls into several ranges leaves partial
 // results (slot = CTA + unit, which increases along the ranges and never repeats) for merge_kernel.
 constexpr int AT_THREADS = 128;
 constexpr int TILE = 128;      // tokens per CTA step, 32 per warp
+constexpr int STAGES = 2;      // per warp
 constexpr float LAZY = 8.f;    // log2: the reference moves when it is exceeded by more
 
 struct Tiles {  // the 128-token tiles of a unit: tile i at i < nsk ? i : lo + i - nsk
@@ -232,7 +240,6 @@ __device__ __forceinline__ Tiles unit_tiles(const Kv8Attn& a, int b) {
   t.n = t.len > 0 ? t.nsk + (t.len - 1) / TILE - t.lo + 1 : 0;
   return t;
 }
-// Tiles of sequences [b0, b1) per (head, row group), summed by one warp's lanes or a single thread.
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -256,47 +263,69 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   return *(const uint32_t*)&h;
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t u) { return __half22float2(*(const __half2*)&u); }
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+
+// Dependent launch: the next kernel of the stream may start its prologue; wait for the one before.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Token (0..7) of row x (0..7) of an 8-row half of a S^T tile = contraction index x of O^T.  d_head 128
+// (128-byte rows, 16-byte chunk c of row t at chunk c ^ t): rows x and x ^ 1 differ in bit 2, so that
+// their K chunks 0-3 (4-7) land in different halves, and rows 0, 2, 4, 6 (1, 3, 5, 7) differ in bits 1-2,
+// so that V chunks 2y and 2y + 1 of the four lanes' tokens never meet.
+template <int DH> __device__ __forceinline__ int slot_token(int x) {
+  return DH == 128 ? ((x >> 2) & 1) | (x & 2) | (((x ^ (x >> 2)) & 1) << 2) : x;
+}
+// Byte offset of byte `at` of row t in a swizzled tile.
+template <int DH> __device__ __forceinline__ int swizzled(int t, int at) {
+  return DH == 128 ? t * 128 + (at ^ ((t & 7) << 4)) : t * 64 + (at ^ (((t >> 1) & 3) << 4));
 }
 
-template <int DH> struct Piece;  // a lane's piece of a V row: DH / 8 bytes
-template <> struct Piece<128> { uint32_t w[4]; };
-template <> struct Piece<64> { uint32_t w[2]; };
-template <int DH> __device__ __forceinline__ Piece<DH> load_piece(const uint8_t* p);
-template <> __device__ __forceinline__ Piece<128> load_piece<128>(const uint8_t* p) {
-  const uint4 v = __ldg((const uint4*)p);
-  return {{v.x, v.y, v.z, v.w}};
-}
-template <> __device__ __forceinline__ Piece<64> load_piece<64>(const uint8_t* p) {
-  const uint2 v = __ldg((const uint2*)p);
-  return {{v.x, v.y}};
-}
+template <int DH> struct AtCfg {
+  static constexpr int HALF = 32 * DH;            // 32 rows of K (or V)
+  static constexpr int WARP = STAGES * 2 * HALF;  // a warp's stages: K, V
+  static constexpr int SMEM = 4 * WARP + 1024;
+};
 
 // NT: groups of 8 query rows; SPLIT: float32 queries and outputs; WT: raw scores go to a.scores.
 template <typename T, int DH, int NT, bool WT>
-__global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(Kv8Attn a) {
+__global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
+    attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Kv8Attn a, int* status) {
+  using namespace sm100;
+  using C = AtCfg<DH>;
   constexpr bool SPLIT = sizeof(T) == 4;
   constexpr int KW = DH / 16;      // 32-bit words of a K row per lane = k-steps of S^T
   constexpr int MT = DH / 16;      // 16-channel tiles of O^T
   constexpr int VW = DH / 32;      // 32-bit words of a V row per lane
   constexpr int RT = 8 * NT;
-  __shared__ float sO[4][RT][DH + 4];
+  constexpr int OLD = DH + 4;      // row stride of the warps' O in shared memory
+  static_assert(RT * OLD * 4 <= C::WARP, "a warp's O fits its stages");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ __align__(8) uint64_t bars[4][STAGES];
   __shared__ float sStat[4][RT][3];  // ml, l, mu of each warp
   __shared__ long long sScan[AT_THREADS / 32];
   __shared__ int sStart[2];
+  __shared__ int sAbort;
+  volatile int* abort = &sAbort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, c4 = lane & 3;
   const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg;  // units per sequence
+  uint8_t* mine = smem + warp * C::WARP;
+  uint64_t* full = bars[warp];
 
+  allow_next_kernel();
+  if (threadIdx.x == 0) {
+    sAbort = 0;
+    for (int i = 0; i < 4; ++i)
+      for (int k = 0; k < STAGES; ++k) mbar_init(&bars[i][k], 1);
+    fence_barrier_init();
+  }
   // this CTA's range of tiles [w0, w1) and the sequence that w0 falls into
   long long total;
   {
     const int per = (a.c.B + AT_THREADS - 1) / AT_THREADS, b0 = min(threadIdx.x * per, a.c.B), b1 = min(b0 + per, a.c.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (long long)unit_tiles(a, b).n * upb;
-    long long inc = mine;
+    long long own = 0;
+    for (int b = b0; b < b1; ++b) own += (long long)unit_tiles(a, b).n * upb;
+    long long inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -304,14 +333,14 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
     }
     if (lane == 31) sScan[warp] = inc;
     __syncthreads();
-    long long before = inc - mine;
+    long long before = inc - own;
     total = 0;
     for (int i = 0; i < AT_THREADS / 32; ++i) {
       if (i < warp) before += sScan[i];
       total += sScan[i];
     }
     const long long share = (total + gridDim.x - 1) / gridDim.x, w0 = share * blockIdx.x;
-    if (w0 >= before && w0 < before + mine) {  // one thread at most
+    if (w0 >= before && w0 < before + own) {  // one thread at most
       long long left = w0 - before;
       int b = b0;
       for (;; ++b) {
@@ -330,15 +359,33 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
   int todo = (int)(w1 - w0), b = sStart[0];
   Tiles ts = unit_tiles(a, b);
   int u = sStart[1] / ts.n, first = sStart[1] % ts.n;  // unit within the sequence, its first tile here
+  int kvit = 0;  // tiles this warp has taken from its stages
+  const uint64_t pol = policy_evict_first();  // the cache is read once
+
+  // lane constants: offsets of its pieces in a 32-row stage
+  int koff[DH / 64], voff[2];
+#pragma unroll
+  for (int q = 0; q < DH / 64; ++q) koff[q] = swizzled<DH>(slot_token<DH>(g8), q * 64 + c4 * 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) voff[i] = swizzled<DH>(slot_token<DH>(2 * c4 + i), g8 * (DH / 8));
 
   while (todo > 0) {
     const int cnt = min(todo, ts.n - first);
     const int g = u / nrg, rg = u % nrg;
     const size_t hd = (size_t)b * a.c.Hkv + g;
-    const uint8_t* kc = (const uint8_t*)a.c.k + hd * a.c.Lmax * DH;
-    const uint8_t* vc = (const uint8_t*)a.c.v + hd * a.c.Lmax * DH;
+    const int row0 = (int)(hd * a.c.Lmax);
     const float* ksc = a.c.ks + hd * a.c.nblk;
     const float* vsc = a.c.vs + hd * a.c.nblk;
+    auto fetch = [&](int it, int st) {  // lane 0: this warp's rows of the segment's tile `it` into stage st
+      const int y = row0 + ts.tile(first + it) * TILE + warp * 32;
+      mbar_expect_tx(&full[st], 2 * C::HALF);
+      tma_load_2d_hint(mine + st * 2 * C::HALF, &tmK, &full[st], 0, y, pol);
+      tma_load_2d_hint(mine + st * 2 * C::HALF + C::HALF, &tmV, &full[st], 0, y, pol);
+    };
+    if (lane == 0) {
+      fence_proxy_async();  // (the stages held this warp's O of the segment before)
+      for (int i = 0; i < STAGES && i < cnt; ++i) fetch(i, (kvit + i) % STAGES);
+    }
 
     // Q^T fragments of row g8 of each group: k-step w holds the channels of bytes 4w..4w+3 of the
     // lane's K pieces; the row is scaled by a power of two to a maximum in [2^7, 2^8)
@@ -351,14 +398,14 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
       const bool in = r < R;
       const T* qr = (const T*)a.q + ((size_t)b * a.n + (in ? r / a.G : 0)) * (size_t)(a.c.Hkv * a.G * DH) +
                     (size_t)(g * a.G + (in ? r % a.G : 0)) * DH;
-      float x[KW][4], m = 0.f;
+      float x[KW / 4][16], m = 0.f;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const int d = (w >> 2) * 64 + c4 * 16 + (w & 3) * 4;
+      for (int q = 0; q < KW / 4; ++q) {
+        load16<T>(qr + q * 64 + c4 * 16, x[q]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[w][i] = in ? to_f<T>(qr[d + i]) : 0.f;
-          m = fmaxf(m, fabsf(x[w][i]));
+        for (int i = 0; i < 16; ++i) {
+          if (!in) x[q][i] = 0.f;
+          m = fmaxf(m, fabsf(x[q][i]));
         }
       }
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -369,7 +416,7 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
       for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float y0 = x[w][2 * i] * down, y1 = x[w][2 * i + 1] * down;
+          const float y0 = x[w >> 2][(w & 3) * 4 + 2 * i] * down, y1 = x[w >> 2][(w & 3) * 4 + 2 * i + 1] * down;
           qf[t][w][i] = pack_h2(y0, y1);
           if constexpr (SPLIT) {
             const float2 h = unpack_h2(qf[t][w][i]);
@@ -399,39 +446,20 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][t][i] = 0.f;
-
-    uint4 kr[2][2][DH / 64];  // [16-token half][token g8 or g8 + 8][64-byte half of the row]
-    Piece<DH> vr[2][4];       // [16-token half][token 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9]
-    float ks[2], vs[2];
-    auto load_k = [&](int j0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ks[h] = __ldg(ksc + min((j0 + 16 * h) / a.c.block, a.c.nblk - 1));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* p = kc + (size_t)min(j0 + 16 * h + 8 * i + g8, a.c.Lmax - 1) * DH + c4 * 16;
-#pragma unroll
-          for (int q = 0; q < DH / 64; ++q) kr[h][i][q] = __ldg((const uint4*)(p + q * 64));
-        }
-      }
-    };
-    auto load_v = [&](int j0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        vs[h] = __ldg(vsc + min((j0 + 16 * h) / a.c.block, a.c.nblk - 1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vr[h][i] = load_piece<DH>(vc + (size_t)min(j0 + 16 * h + 2 * c4 + (i & 1) + 8 * (i >> 1), a.c.Lmax - 1) * DH +
-                                    g8 * (DH / 8));
-      }
-    };
     auto sees = [&](int j, int p) { return j <= p && (!a.window || j > p - a.window || j < a.sinks); };
 
-    load_k(ts.tile(first) * TILE + warp * 32);
-    load_v(ts.tile(first) * TILE + warp * 32);
-    for (int it = 0; it < cnt; ++it) {
-      const int j0 = ts.tile(first + it) * TILE + warp * 32;
-      const int jn = it + 1 < cnt ? ts.tile(first + it + 1) * TILE + warp * 32 : -1;
+    for (int it = 0; it < cnt; ++it, ++kvit) {
+      const int st = kvit % STAGES, j0 = ts.tile(first + it) * TILE + warp * 32;
+      const uint8_t* sk = mine + st * 2 * C::HALF;
+      const uint8_t* sv = sk + C::HALF;
+      float kf[2], ev[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tb = min((j0 + 16 * h) / a.c.block, a.c.nblk - 1);
+        kf[h] = __ldg(ksc + tb);
+        ev[h] = (float)exp_of(__ldg(vsc + tb));
+      }
+      if (!mbar_wait_warp(&full[st], (kvit / STAGES) & 1, abort, status)) break;
       // S^T of 32 tokens
       float s[2][NT][4];
 #pragma unroll
@@ -441,37 +469,33 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[h][t][i] = 0.f;
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const uint4 &x0 = kr[h][0][w >> 2], &x1 = kr[h][1][w >> 2];
-          const uint32_t y0 = (w & 3) == 0 ? x0.x : (w & 3) == 1 ? x0.y : (w & 3) == 2 ? x0.z : x0.w;
-          const uint32_t y1 = (w & 3) == 0 ? x1.x : (w & 3) == 1 ? x1.y : (w & 3) == 2 ? x1.z : x1.w;
-          const uint32_t a0 = e4m3x2_to_h2(y0), a1 = e4m3x2_to_h2(y1), a2 = e4m3x2_to_h2(y0 >> 16),
-                         a3 = e4m3x2_to_h2(y1 >> 16);
+        for (int q = 0; q < DH / 64; ++q) {
+          const uint4 x0 = *(const uint4*)(sk + h * 16 * DH + koff[q]), x1 = *(const uint4*)(sk + (h * 16 + 8) * DH + koff[q]);
+          const uint32_t y0[4] = {x0.x, x0.y, x0.z, x0.w}, y1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma16816(s[h][t], a0, a1, a2, a3, qf[t][w][0], qf[t][w][1]);
-            if constexpr (SPLIT) mma16816(s[h][t], a0, a1, a2, a3, ql[t][w][0], ql[t][w][1]);
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = e4m3x2_to_h2(y0[w]), a1 = e4m3x2_to_h2(y1[w]), a2 = e4m3x2_to_h2(y0[w] >> 16),
+                           a3 = e4m3x2_to_h2(y1[w] >> 16);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816(s[h][t], a0, a1, a2, a3, qf[t][q * 4 + w][0], qf[t][q * 4 + w][1]);
+              if constexpr (SPLIT) mma16816(s[h][t], a0, a1, a2, a3, ql[t][q * 4 + w][0], ql[t][q * 4 + w][1]);
+            }
           }
         }
       }
-      const float kf[2] = {ks[0], ks[1]};
-      if (jn >= 0) load_k(jn);
 
-      // scores in log2 units; hidden ones -inf
+      // hidden scores -inf; s[h][t][i]: token j0 + 16 h + 8 (i / 2) + slot_token(g8), row 2 c4 + i % 2
       const bool edge = j0 + 31 > p_lo || (a.window && j0 <= p_hi - a.window && j0 + 31 >= a.sinks);  // warp-uniform
-      const float ev[2] = {(float)exp_of(vs[0]), (float)exp_of(vs[1])};
-      bool over = false;
+      if (edge) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // token j0 + 16 h + g8 + 8 (i / 2), row 2 c4 + i % 2
-            float x = s[h][t][i] * (kf[h] * rf[t][i & 1]);
-            if (edge && !sees(j0 + 16 * h + g8 + 8 * (i >> 1), qpos[t][i & 1])) x = -INFINITY;
-            s[h][t][i] = x;
-            over |= x > ml[t][i & 1] + LAZY || x + ev[h] > mu[t][i & 1] + LAZY;
-          }
+            for (int i = 0; i < 4; ++i)
+              if (!sees(j0 + 16 * h + 8 * (i >> 1) + slot_token<DH>(g8), qpos[t][i & 1])) s[h][t][i] = -INFINITY;
+      }
       if constexpr (WT) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -479,38 +503,49 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int j = j0 + 16 * h + g8 + 8 * (i >> 1), r = rg * RT + t * 8 + 2 * c4 + (i & 1);
-              if (j < ts.len && r < R) a.scores[(hd * a.c.Lmax + j) * R + r] = s[h][t][i];
+              const int j = j0 + 16 * h + 8 * (i >> 1) + slot_token<DH>(g8), r = rg * RT + t * 8 + 2 * c4 + (i & 1);
+              const float x = s[h][t][i] == -INFINITY ? -INFINITY : s[h][t][i] * (kf[h] * rf[t][i & 1]);
+              if (j < ts.len && r < R) a.scores[(hd * a.c.Lmax + j) * R + r] = x;
             }
       }
+      // scores in log2 units are s * f; two references per row, for the sum (ml) and, with the exponent
+      // ev of V's block scale added, for the products with V's codes (mu)
+      bool over = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            over |= fmaxf(s[h][t][k], s[h][t][k + 2]) * (kf[h] * rf[t][k]) > fminf(ml[t][k], mu[t][k] - ev[h]) + LAZY;
       if (__any_sync(0xffffffffu, over)) {  // move the references to the tile's maxima
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int k = 0; k < 2; ++k) {
             float x = -INFINITY, y = -INFINITY;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float z = fmaxf(s[h][t][i], s[h][t][i + 2]);
-              x = fmaxf(x, z);
-              y = fmaxf(y, z + ev[h]);
+              const float z = fmaxf(s[h][t][k], s[h][t][k + 2]), v = z == -INFINITY ? z : z * (kf[h] * rf[t][k]);
+              x = fmaxf(x, v);
+              y = fmaxf(y, v + ev[h]);
             }
 #pragma unroll
-            for (int k = 4; k < 32; k <<= 1) {
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, k));
+            for (int d = 4; d < 32; d <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
             }
-            if (x > ml[t][i]) {
-              l[t][i] *= ex2f(ml[t][i] - x);
-              ml[t][i] = x;
+            if (x > ml[t][k]) {
+              l[t][k] *= ex2(ml[t][k] - x);
+              ml[t][k] = x;
             }
-            if (y > mu[t][i]) {
-              const float f = ex2f(mu[t][i] - y);
-              mu[t][i] = y;
+            if (y > mu[t][k]) {
+              const float f = ex2(mu[t][k] - y);
+              mu[t][k] = y;
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                o[m][t][i] *= f;
-                o[m][t][i + 2] *= f;
+                o[m][t][k] *= f;
+                o[m][t][k + 2] *= f;
               }
             }
           }
@@ -526,10 +561,10 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
             float y[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float x = s[h][t][2 * i + k];
+              const float x = s[h][t][2 * i + k], f = kf[h] * rf[t][k];
               const bool hid = edge && x == -INFINITY;
-              y[k] = hid ? 0.f : ex2f(x + ev[h] - mu[t][k]);
-              l[t][k] += hid ? 0.f : ex2f(x - ml[t][k]);
+              y[k] = hid ? 0.f : ex2(fmaf(x, f, ev[h] - mu[t][k]));
+              l[t][k] += hid ? 0.f : ex2(fmaf(x, f, -ml[t][k]));
             }
             const uint32_t hi = pack_h2(y[0], y[1]);
             pf[h][t][i] = transpose8x8(hi);
@@ -538,13 +573,26 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
               pl[h][t][i] = transpose8x8(pack_h2(y[0] - f.x, y[1] - f.y));
             }
           }
-      if (edge) {
-        // a hidden token's P is 0, but 0 * NaN is not: its NaN codes are cleared, and the rows that do
-        // see such a token get their NaN directly
+      // O^T += V^T P^T; channel tile m holds the channels 2m and 2m + 1 of each lane's piece; piece i is
+      // of contraction index 2 c4 + i % 2 + 8 (i / 2)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t nan[4];  // bit d: channel d of this lane's piece of token slot i is NaN
-          uint32_t any = 0;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t vr[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* p = sv + (h * 16 + 8 * (i >> 1)) * DH + voff[i & 1];
+          if constexpr (DH == 128) {
+            const uint4 x = *(const uint4*)p;
+            vr[i][0] = x.x; vr[i][1] = x.y; vr[i][2] = x.z; vr[i][3] = x.w;
+          } else {
+            const uint2 x = *(const uint2*)p;
+            vr[i][0] = x.x; vr[i][1] = x.y;
+          }
+        }
+        if (edge) {
+          // a hidden token's P is 0, but 0 * NaN is not: NaN codes are cleared, and the rows that do see
+          // such a token get their NaN directly
+          uint32_t nan[4], any = 0;  // bit d: channel d of this lane's piece i is NaN
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             nan[i] = 0;
@@ -552,9 +600,9 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
             for (int w = 0; w < VW; ++w)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (((vr[h][i].w[w] >> (8 * k)) & 0x7f) == 0x7f) {
+                if (((vr[i][w] >> (8 * k)) & 0x7f) == 0x7f) {
                   nan[i] |= 1u << (4 * w + k);
-                  vr[h][i].w[w] &= ~(0xffu << (8 * k));
+                  vr[i][w] &= ~(0xffu << (8 * k));
                 }
             any |= nan[i];
           }
@@ -563,7 +611,7 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t bits = __shfl_sync(0xffffffffu, nan[i], (lane & ~3) | src);
-                const int j = j0 + 16 * h + 2 * src + (i & 1) + 8 * (i >> 1);
+                const int j = j0 + 16 * h + 8 * (i >> 1) + slot_token<DH>(2 * src + (i & 1));
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -577,15 +625,11 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
               }
           }
         }
-      }
-      // O^T += V^T P^T; channel tile m holds the channels 2m and 2m + 1 of each lane's piece
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const uint32_t sel = (m & 1) ? 0x7362u : 0x5140u;
-          const uint32_t x = __byte_perm(vr[h][0].w[m >> 1], vr[h][1].w[m >> 1], sel);
-          const uint32_t y = __byte_perm(vr[h][2].w[m >> 1], vr[h][3].w[m >> 1], sel);
+          const uint32_t x = __byte_perm(vr[0][m >> 1], vr[1][m >> 1], sel);
+          const uint32_t y = __byte_perm(vr[2][m >> 1], vr[3][m >> 1], sel);
           const uint32_t a0 = e4m3x2_to_h2(x), a1 = e4m3x2_to_h2(x >> 16), a2 = e4m3x2_to_h2(y), a3 = e4m3x2_to_h2(y >> 16);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -593,28 +637,34 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
             if constexpr (SPLIT) mma16816(o[m][t], a0, a1, a2, a3, pl[h][t][0], pl[h][t][1]);
           }
         }
-      if (jn >= 0) load_v(jn);
+      }
+      __syncwarp();
+      if (lane == 0 && it + STAGES < cnt) fetch(it + STAGES, st);
     }
 
-    // join the four warps
+    // join the four warps, each one's O in its own stages (none of its copies is in flight)
+    float* so = (float*)mine;
+    if (!*abort) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = l[t][i];
+        for (int i = 0; i < 2; ++i) {
+          float x = l[t][i];
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-        const int r = t * 8 + 2 * c4 + i;
-        if (g8 == 0) {
-          sStat[warp][r][0] = ml[t][i];
-          sStat[warp][r][1] = x;
-          sStat[warp][r][2] = mu[t][i];
+          for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+          const int r = t * 8 + 2 * c4 + i;
+          if (g8 == 0) {
+            sStat[warp][r][0] = ml[t][i];
+            sStat[warp][r][1] = x;
+            sStat[warp][r][2] = mu[t][i];
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            *(float2*)&so[r * OLD + g8 * (DH / 8) + 2 * m] = make_float2(o[m][t][i], o[m][t][i + 2]);
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          *(float2*)&sO[warp][r][g8 * (DH / 8) + 2 * m] = make_float2(o[m][t][i], o[m][t][i + 2]);
-      }
+    }
     __syncthreads();
+    if (*abort) break;
     const bool whole = first == 0 && cnt == ts.n;
     const size_t slot = (size_t)blockIdx.x + (size_t)b * upb + u;
     for (int at = threadIdx.x; at < RT * (DH / 4); at += AT_THREADS) {
@@ -630,16 +680,14 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float fl = sStat[w][r][0] == -INFINITY ? 0.f : ex2f(sStat[w][r][0] - L);
-        const float fu = sStat[w][r][2] == -INFINITY ? 0.f : ex2f(sStat[w][r][2] - U);
-        sum += sStat[w][r][1] * (sStat[w][r][1] == 0.f ? 1.f : fl);
-        const float4 y = *(const float4*)&sO[w][r][d];
         // (a warp that saw nothing holds zeros, or the NaN of a NaN score: added as it is)
-        const float f = sStat[w][r][2] == -INFINITY ? 1.f : fu;
+        sum += sStat[w][r][0] == -INFINITY ? sStat[w][r][1] : sStat[w][r][1] * ex2(sStat[w][r][0] - L);
+        const float4 y = *(const float4*)((const float*)(smem + w * C::WARP) + r * OLD + d);
+        const float f = sStat[w][r][2] == -INFINITY ? 1.f : ex2(sStat[w][r][2] - U);
         x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
       }
       if (whole) {
-        const float f = sum == 0.f ? 0.f : ex2f(U - L) / sum;  // a row that sees nothing is 0
+        const float f = sum == 0.f ? 0.f : ex2(U - L) / sum;  // a row that sees nothing is 0
         T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) +
                  (size_t)(g * a.G + row % a.G) * DH + d;
         out[0] = from_f<T>(x.x * f); out[1] = from_f<T>(x.y * f); out[2] = from_f<T>(x.z * f); out[3] = from_f<T>(x.w * f);
@@ -659,60 +707,112 @@ __global__ void __launch_bounds__(AT_THREADS, NT == 1 ? 3 : 2) attention_kernel(
       while (ts.n == 0);
     }
   }
+  if (threadIdx.x == 0) linger_after_abort(abort);  // a wait ran out: this CTA's copies land first
 }
 
-// Joins the partial results of one query row of one unit; a unit without tiles gives 0.  One CTA of DH
-// threads (a channel each) per (unit, row).
+// Joins the partial results of one query row of one unit; a unit without tiles gives 0.  One CTA of eight
+// warps per (unit, row): the records' maxima first, then every warp adds a share of the records.
+constexpr int MG_THREADS = 256;
+constexpr int MG_MOST = 1024;  // records of a unit = CTAs of the attention at most
 template <typename T, int DH, bool WT>
-__global__ void __launch_bounds__(DH) merge_kernel(Kv8Attn a, int RT, int grid) {
-  __shared__ long long s[DH / 32][2];
+__global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, int grid) {
+  using sm100::ex2;
+  constexpr int PER = DH / 32;  // channels per lane
+  __shared__ long long sCount[MG_THREADS / 32][2];
+  __shared__ float sMax[MG_THREADS / 32][2], sSum[MG_THREADS / 32];
+  __shared__ float sFac[MG_MOST];
+  __shared__ float sX[MG_THREADS / 32][DH];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg;
   const int row = blockIdx.x, g = blockIdx.y, b = blockIdx.z, rg = row / RT, r = row % RT, u = g * nrg + rg;
+  const size_t hd = (size_t)b * a.c.Hkv + g;
+  T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) + (size_t)(g * a.G + row % a.G) * DH;
+  allow_next_kernel();
   const Tiles ts = unit_tiles(a, b);
+  if (ts.n == 0) {
+    wait_previous_kernel();
+    if (threadIdx.x < DH) out[threadIdx.x] = from_f<T>(0.f);
+    return;
+  }
   long long before = 0, total = 0;
-  for (int i = threadIdx.x; i < a.c.B; i += DH) {
+  for (int i = threadIdx.x; i < a.c.B; i += MG_THREADS) {
     const long long t = (long long)unit_tiles(a, i).n * upb;
     total += t;
     if (i < b) before += t;
   }
   before = warp_sum_ll(before);
   total = warp_sum_ll(total);
-  if ((threadIdx.x & 31) == 0) {
-    s[threadIdx.x >> 5][0] = before;
-    s[threadIdx.x >> 5][1] = total;
+  if (lane == 0) {
+    sCount[warp][0] = before;
+    sCount[warp][1] = total;
   }
   __syncthreads();
   before = total = 0;
-  for (int i = 0; i < DH / 32; ++i) {
-    before += s[i][0];
-    total += s[i][1];
-  }
-  const size_t hd = (size_t)b * a.c.Hkv + g;
-  T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) + (size_t)(g * a.G + row % a.G) * DH +
-           threadIdx.x;
-  if (ts.n == 0) {
-    *out = from_f<T>(0.f);
-    return;
+#pragma unroll
+  for (int i = 0; i < MG_THREADS / 32; ++i) {
+    before += sCount[i][0];
+    total += sCount[i][1];
   }
   const long long share = (total + grid - 1) / grid, start = before + (long long)u * ts.n, end = start + ts.n - 1;
-  const int c0 = (int)(start / share), c1 = (int)(end / share);
-  if (c0 == c1) return;  // written whole by its CTA
-  const size_t slot0 = (size_t)b * upb + u;
-  float L = -INFINITY, U = -INFINITY, sum = 0.f, x = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const float* rec = a.part + ((slot0 + c) * RT + r) * (DH + 4);
-    L = fmaxf(L, rec[0]);
-    U = fmaxf(U, rec[2]);
+  const int c0 = (int)(start / share), nrec = (int)(end / share) - c0 + 1;
+  // every CTA waits, so that this kernel's end means the attention's too
+  wait_previous_kernel();
+  if (nrec == 1) return;  // written whole by its CTA
+  const float* rec0 = a.part + (((size_t)b * upb + u + c0) * RT + r) * (DH + 4);
+  const size_t step = (size_t)RT * (DH + 4);
+  float L = -INFINITY, U = -INFINITY;
+  for (int i = threadIdx.x; i < nrec; i += MG_THREADS) {
+    const float4 h = *(const float4*)(rec0 + i * step);
+    L = fmaxf(L, h.x);
+    U = fmaxf(U, h.z);
   }
-  for (int c = c0; c <= c1; ++c) {
-    const float* rec = a.part + ((slot0 + c) * RT + r) * (DH + 4);
-    const float l = rec[1];
-    sum += rec[0] == -INFINITY ? l : l * ex2f(rec[0] - L);
-    const float y = rec[4 + threadIdx.x];
-    x += rec[2] == -INFINITY ? y : y * ex2f(rec[2] - U);
+  L = warp_max(L);
+  U = warp_max(U);
+  if (lane == 0) {
+    sMax[warp][0] = L;
+    sMax[warp][1] = U;
   }
-  *out = from_f<T>(sum == 0.f ? 0.f : x * (ex2f(U - L) / sum));
-  if (WT && threadIdx.x == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MG_THREADS / 32; ++i) {
+    L = fmaxf(L, sMax[i][0]);
+    U = fmaxf(U, sMax[i][1]);
+  }
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < nrec; i += MG_THREADS) {
+    const float4 h = *(const float4*)(rec0 + i * step);
+    sum += h.x == -INFINITY ? h.y : h.y * ex2(h.x - L);
+    sFac[i] = h.z == -INFINITY ? 1.f : ex2(h.z - U);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) sSum[warp] = sum;
+  __syncthreads();
+  float x[PER] = {};
+  for (int i = warp; i < nrec; i += MG_THREADS / 32) {
+    const float f = sFac[i];
+    const float* p = rec0 + i * step + 4 + lane * PER;
+    if constexpr (PER == 4) {
+      const float4 y = *(const float4*)p;
+      x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
+    } else {
+      const float2 y = *(const float2*)p;
+      x[0] += y.x * f; x[1] += y.y * f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < PER; ++k) sX[warp][lane * PER + k] = x[k];
+  __syncthreads();
+  if (threadIdx.x < DH) {
+    float v = 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < MG_THREADS / 32; ++i) {
+      v += sX[i][threadIdx.x];
+      sum += sSum[i];
+    }
+    out[threadIdx.x] = from_f<T>(sum == 0.f ? 0.f : v * (ex2(U - L) / sum));
+    if (WT && threadIdx.x == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
+  }
 }
 
 // weights[b][g][j] += sum over the query rows of KV head g of their softmax weight of token j, from the
@@ -720,6 +820,7 @@ __global__ void __launch_bounds__(DH) merge_kernel(Kv8Attn a, int RT, int grid) 
 __global__ void __launch_bounds__(128) weights_kernel(Kv8Attn a) {
   const int b = blockIdx.z, g = blockIdx.y;
   const Tiles ts = unit_tiles(a, b);
+  wait_previous_kernel();
   if (blockIdx.x >= ts.n) return;
   const int j = ts.tile(blockIdx.x) * TILE + threadIdx.x, R = a.G * a.n;
   if (j >= ts.len) return;
@@ -730,7 +831,7 @@ __global__ void __launch_bounds__(128) weights_kernel(Kv8Attn a) {
   for (int r = 0; r < R; ++r) {
     const float2 x = st[r];
     const float y = s[r];
-    if (y != -INFINITY) w += ex2f(y - x.x) / x.y;
+    if (y != -INFINITY) w += sm100::ex2(y - x.x) / x.y;
   }
   a.weights[hd * a.c.Lmax + j] += w;
 }
@@ -902,19 +1003,35 @@ cudaError_t kv8_read(const Kv8Args& a, const int* first, const int* rows, int n,
   return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
 }
 
-// Groups of 8 query rows per unit: a second group shares the cache's bytes and conversions, but takes
-// registers that otherwise hold a third CTA per SM.
+// Groups of 8 query rows per unit: a second one shares the cache's bytes and conversions.
 static int kv8_groups(int R) { return R <= 8 ? 1 : 2; }
-static int kv8_grid(int R) {
+// CTAs: as many as the registers and the stages (d_head 128: 65 KB a CTA) let stay resident.
+static int kv8_grid(int R, int dh) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms * (kv8_groups(R) == 1 ? 3 : 2);
+  const int grid = sms * (kv8_groups(R) == 2 && dh == 128 ? 2 : 3);
+  return grid < kv8::MG_MOST ? grid : kv8::MG_MOST;
+}
+
+// A launch that may start while the kernel before it in the stream still runs (it waits for it itself).
+template <typename... P, typename... A>
+static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t* stats, size_t* scores) {
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t R = (size_t)G * n, RT = 8 * kv8_groups((int)R), nrg = (R + RT - 1) / RT;
-  size_t o = al((kv8_grid((int)R) + (size_t)c.B * c.Hkv * nrg) * RT * (c.dh + 4) * 4);
+  size_t o = al((kv8_grid((int)R, c.dh) + (size_t)c.B * c.Hkv * nrg) * RT * (c.dh + 4) * 4);
   *stats = o;
   if (weights) o += al((size_t)c.B * c.Hkv * R * 8);
   *scores = o;
@@ -922,19 +1039,26 @@ size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t
   return o;
 }
 
-cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, cudaStream_t s) {
-  const int R = a.G * a.n, nt = kv8_groups(R), grid = kv8_grid(R);
+cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream_t s) {
+  const int R = a.G * a.n, nt = kv8_groups(R), grid = kv8_grid(R, a.c.dh);
+  const long long rows = (long long)a.c.B * a.c.Hkv * a.c.Lmax;
+  CUtensorMap tk, tv;
+  cudaError_t me = make_tmap_u8(&tk, a.c.k, rows, a.c.dh, 32);
+  if (me == cudaSuccess) me = make_tmap_u8(&tv, a.c.v, rows, a.c.dh, 32);
+  if (me != cudaSuccess) return me;
   auto run = [&](auto type, auto dh, auto nts, auto wt) {
     using T = decltype(type);
     constexpr int DH = decltype(dh)::value, NT = decltype(nts)::value;
     constexpr bool WT = decltype(wt)::value;
-    kv8::attention_kernel<T, DH, NT, WT><<<grid, kv8::AT_THREADS, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    auto* kernel = kv8::attention_kernel<T, DH, NT, WT>;
+    constexpr int smem = kv8::AtCfg<DH>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kv8::merge_kernel<T, DH, WT><<<dim3(R, a.c.Hkv, a.c.B), DH, 0, s>>>(a, 8 * NT, grid);
-    if ((e = cudaGetLastError()) != cudaSuccess || !WT) return e;
-    kv8::weights_kernel<<<dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, 0, s>>>(a);
-    return cudaGetLastError();
+    kernel<<<grid, kv8::AT_THREADS, smem, s>>>(tk, tv, a, status);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dependent(kv8::merge_kernel<T, DH, WT>, dim3(R, a.c.Hkv, a.c.B), kv8::MG_THREADS, s, a, 8 * NT, grid);
+    if (e != cudaSuccess || !WT) return e;
+    return launch_dependent(kv8::weights_kernel, dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, s, a);
   };
   auto with_wt = [&](auto type, auto dh, auto nts) {
     return a.weights ? run(type, dh, nts, std::true_type()) : run(type, dh, nts, std::false_type());
