@@ -102,7 +102,8 @@ int check_kv8(const char* who, const mka_kv8_config* c, const mka_kv8_cache* cac
       (long long)c->batch * c->n_kv_heads * c->max_positions > 0x7fffffffLL - 128)
     return fail(MKA_ERR_UNSUPPORTED, "%s: batch, heads or max_positions too large", who);
   o->a = {nullptr, nullptr, nullptr, nullptr, c->batch, c->n_kv_heads, c->d_head, c->max_positions, c->block,
-          (c->max_positions + c->block - 1) / c->block};
+          (c->max_positions + c->block - 1) / c->block,
+          c->block == 16 ? 4 : c->block == 32 ? 5 : c->block == 64 ? 6 : 7};
   o->Hq = c->n_q_heads;
   o->G = c->n_q_heads / c->n_kv_heads;
   o->bf16 = c->dtype == MKA_BF16;

@@ -284,6 +284,7 @@ struct Kv8Args {
   void *k, *v;       // e4m3 codes [B][Hkv][Lmax][dh], 16-byte aligned
   float *ks, *vs;    // scales [B][Hkv][nblk], powers of two
   int B, Hkv, dh, Lmax, block, nblk;  // block: 16, 32, 64 or 128; nblk = ceil(Lmax / block)
+  int lb;                             // log2(block)
 };
 // Rows of K and V (head g of row t of sequence b at b * batch_stride + t * row_stride + g * dh) to
 // positions pos[b].. of the cache, count[b] (null: n) of them; see mka_kv8_append.

@@ -31,11 +31,11 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ int exp_of(float p2) { return (int)(__float_as_uint(p2) >> 23) - 127; }
 
-// Two values to e4m3 (a in the low byte): round to nearest even; NaN and infinities become NaN.
+// x, an infinity as NaN.
+__device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
+// Two values to e4m3 (a in the low byte): round to nearest even.
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   uint16_t r;
-  a = isfinite(a) ? a : kQuietNaN;
-  b = isfinite(b) ? b : kQuietNaN;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
@@ -97,19 +97,43 @@ __device__ __forceinline__ void decode16(const uint4& c, float f, float (&x)[16]
     x[4 * k] = a.x * f; x[4 * k + 1] = a.y * f; x[4 * k + 2] = b.x * f; x[4 * k + 3] = b.y * f;
   }
 }
+// 16 values times a power of two to codes; infinities become NaN.
 __device__ __forceinline__ uint4 encode16(const float (&x)[16], float inv) {
   uint32_t w[4];
+  float y[16];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    w[k] = to_e4m3x2(x[4 * k] * inv, x[4 * k + 1] * inv) | (to_e4m3x2(x[4 * k + 2] * inv, x[4 * k + 3] * inv) << 16);
+  for (int i = 0; i < 16; ++i) y[i] = fmaf(x[i], inv, x[i] * 0.f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = to_e4m3x2(y[4 * k], y[4 * k + 1]) | (to_e4m3x2(y[4 * k + 2], y[4 * k + 3]) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // max |x| over the finite values.
 __device__ __forceinline__ float amax16(const float (&x)[16]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, isfinite(x[i]) ? fabsf(x[i]) : 0.f);
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(finite_or_nan(x[i])));
   return m;
+}
+// Codes of a scale 2^-d times as large: value * 2^d rounded once.  In half precision: a code times 2^d is
+// exact there wherever it does not round to 0 (below 2^-10 it does, and a code of 4 significant bits that
+// stays above is a multiple of 2^-14 at least), and the caller's scale keeps it within 448.
+__device__ __forceinline__ uint4 rescale16(const uint4& c, int d) {
+  d = min(max(d, -24), 18);
+  const int d1 = min(max(d, -14), 15);
+  const __half2 f1 = __float2half2_rn(pow2(d1)), f2 = __float2half2_rn(pow2(d - d1));
+  uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint16_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t h = e4m3x2_to_h2(w[k] >> (16 * i));
+      const __half2 y = __hmul2(__hmul2(*(const __half2*)&h, f1), f2);
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r[i]) : "r"(*(const uint32_t*)&y));
+    }
+    w[k] = r[0] | (uint32_t)r[1] << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Maximum over a block of NT threads (every thread gets it).
@@ -141,7 +165,7 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* 
     if (threadIdx.x == 0) set_status(status, p < 0 ? kStatusBounds : kStatusCapacity);
     return;
   }
-  const int tb = p / a.block + blockIdx.x, t0 = tb * a.block;
+  const int tb = (p >> a.lb) + blockIdx.x, t0 = tb * a.block;
   const int lo = max(p, t0), hi = min(p + c, t0 + a.block);  // new rows of this token block
   if (lo >= hi) return;
   uint8_t* codes = (uint8_t*)(kv ? a.v : a.k) + ((size_t)b * a.Hkv + g) * a.Lmax * DH;
@@ -168,12 +192,9 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* 
     if (ch < nch) *(uint4*)(codes + (size_t)(lo + ch / CPR) * DH + ch % CPR * 16) = encode16(v[i], inv);
   }
   if (lo > t0 && e != exp_of(old)) {
-    const float f = pow2(max(-126, exp_of(old) - e));  // below 2^-126 every code rounds to 0 anyway
     for (int ch = threadIdx.x; ch < (lo - t0) * CPR; ch += AP_THREADS) {
       uint4* at = (uint4*)(codes + (size_t)(t0 + ch / CPR) * DH + ch % CPR * 16);
-      float y[16];
-      decode16(*at, f, y);
-      *at = encode16(y, 1.f);
+      *at = rescale16(*at, exp_of(old) - e);
     }
   }
   if (threadIdx.x == 0) *scale = pow2(e);
@@ -197,7 +218,7 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
   if (row >= r) return;
   const size_t hd = (size_t)b * a.Hkv + g;
   const uint8_t* codes = (const uint8_t*)(kv ? a.v : a.k) + (hd * a.Lmax + f + row) * DH + ch * 16;
-  const float s = (kv ? a.vs : a.ks)[hd * a.nblk + (f + row) / a.block];
+  const float s = (kv ? a.vs : a.ks)[hd * a.nblk + ((f + row) >> a.lb)];
   float x[16];
   decode16(*(const uint4*)codes, s, x);
   store16<T>((kv ? v_out : k_out) + (size_t)b * batch_stride + (size_t)row * row_stride + g * DH + ch * 16, x);
@@ -455,7 +476,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
       float kf[2], ev[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int tb = min((j0 + 16 * h) / a.c.block, a.c.nblk - 1);
+        const int tb = min((j0 + 16 * h) >> a.c.lb, a.c.nblk - 1);
         kf[h] = __ldg(ksc + tb);
         ev[h] = (float)exp_of(__ldg(vsc + tb));
       }
@@ -839,120 +860,274 @@ __global__ void __launch_bounds__(128) weights_kernel(Kv8Attn a) {
 // ============================================================================ eviction
 // Order of the weights as unsigned integers: larger float, larger key (NaN above infinity).
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);  // -0 and 0 are equal
-  return isnan(w) ? 0xffffffffu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.f);  // -0 and 0 are equal
+  return w != w ? 0xffffffffu : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head): four passes of 8 bits find the key of the last kept token among the
-// middle ones [first, len - recent), then one pass in index order writes the kept tokens: every forced
-// one, every key above the found one, and the first `ties` with exactly that key.
-constexpr int SEL_THREADS = 1024;
-__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weights, int Lmax, int Hkv, const int* lens,
+// The kept positions.  A cluster of CTAs per (sequence, KV head); every lane owns KPT consecutive
+// positions (a warp 32 KPT, a CTA 1024 KPT, rounds of them where the cluster's share is longer than that).
+// Three passes of 11, 11 and 10 bits find the key of the last kept token among the middle ones
+// [first, len - recent): each counts the digits of the keys that match the digits found so far, and the
+// CTAs add each other's counts through distributed shared memory.  Then everyone counts what it keeps --
+// forced tokens, keys above the found one, and of those equal to it the first `need` in position order --
+// and after a prefix sum over lanes, warps and CTAs writes it in order.  Keys are loaded coalesced and
+// turned to their owners through shared memory; a lane's matches are bits of one word, so that a token
+// costs a few instructions a pass (SELECT_NOTE).
+constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32, SEL_BINS = 2048, SEL_CLUSTER = 8;
+constexpr int KPT = 16;                     // positions per lane and round
+constexpr int SEL_ROUND = SEL_THREADS * KPT;
+constexpr int SEL_PITCH = 32 * (KPT + 1);   // a warp's keys in shared memory, one word of padding per lane
+constexpr int SEL_SMEM = SEL_WARPS * SEL_PITCH * 4;
+
+// Two neighbouring ints of this CTA's shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ int2 load_remote2(const int* p, uint32_t rank) {
+  int2 v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %2, %3;\n\tld.shared::cluster.v2.b32 {%0, %1}, [r];\n\t}"
+               : "=r"(v.x), "=r"(v.y) : "r"(sm100::smem_u32(p)), "r"(rank) : "memory");
+  return v;
+}
+__device__ __forceinline__ int warp_excl(int v, int lane) {  // exclusive prefix sum over the lanes
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x - v;
+}
+
+// Bits [lo, hi) of a word of KPT bits, bounds clamped.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = min(max(lo, 0), KPT);
+  hi = min(max(hi, lo), KPT);
+  return ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+}
+
+__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weights, int Lmax, int Hkv, int CL, const int* lens,
                                                              int keep, int first, int recent, int* kept, int* lens2,
                                                              float* weights2, int L2max) {
-  __shared__ int hist[256];
-  __shared__ int sh[4];
-  __shared__ int wsum[2][SEL_THREADS / 32];
-  const int hd = blockIdx.x, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  extern __shared__ uint32_t skeys[];
+  __shared__ __align__(8) int hist[SEL_BINS];
+  __shared__ __align__(8) int sTot[2];
+  __shared__ int sWarp[2][SEL_WARPS], sPick[2];
+  const int hd = blockIdx.x / CL, rank = blockIdx.x % CL, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int len = min(max(lens[b], 0), Lmax);
   const float* w = weights + (size_t)hd * Lmax;
   int* out = kept + (size_t)hd * keep;
   float* w2 = weights2 ? weights2 + (size_t)hd * L2max : nullptr;
-  if (threadIdx.x == 0 && hd % Hkv == 0) lens2[b] = min(len, keep);
-  if (len <= keep) {  // all of a short sequence
-    for (int i = threadIdx.x; i < keep; i += SEL_THREADS) {
+  allow_next_kernel();
+  if (threadIdx.x == 0 && rank == 0 && hd % Hkv == 0) lens2[b] = min(len, keep);
+  if (len <= keep) {  // all of a short sequence (every CTA of the cluster takes this way)
+    for (int i = rank * SEL_THREADS + threadIdx.x; i < keep; i += CL * SEL_THREADS) {
       out[i] = i < len ? i : -1;
       if (w2 && i < len) w2[i] = w[i];
     }
     return;
   }
+  // this CTA's positions [cb, ce), in rounds of SEL_ROUND; a lane's of round q start at cb + q SEL_ROUND +
+  // (32 warp + lane) KPT
+  const int share = ((len + CL - 1) / CL + SEL_WARPS * KPT - 1) / (SEL_WARPS * KPT) * (SEL_WARPS * KPT);
+  const int cb = min(rank * share, len), ce = min(cb + share, len), rounds = (ce - cb + SEL_ROUND - 1) / SEL_ROUND;
   const int m0 = first, m1 = len - recent;
+  uint32_t* mine = skeys + warp * SEL_PITCH;
+  const uint32_t* own = mine + lane * (KPT + 1);
+  // a warp's keys of round q into shared memory (whole warp)
+  auto load = [&](int q) {
+    const int wb = cb + q * SEL_ROUND + warp * 32 * KPT;
+    float f[KPT];
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) f[j] = wb + j * 32 + lane < ce ? w[wb + j * 32 + lane] : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const int x = j * 32 + lane;
+      mine[x + x / KPT] = weight_key(f[j]);
+    }
+    __syncwarp();
+  };
+  const bool once = rounds <= 1;  // the keys stay in shared memory from pass to pass
+  if (once) load(0);
   int need = keep - first - recent;  // of the middle tokens; fewer than there are
-  uint32_t prefix = 0;
-  for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+  const bool none = need == 0;
+  uint32_t prefix = 0, match = 0;  // match (once): this lane's middle positions that match the digits so far
+  for (int pass = 0; pass < 3 && !none; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    const uint32_t mask = (1u << bits) - 1;
+    for (int i = threadIdx.x; i < SEL_BINS; i += SEL_THREADS) hist[i] = 0;
     __syncthreads();
-    for (int i = m0 + threadIdx.x; i < m1; i += SEL_THREADS) {
-      const uint32_t k = weight_key(w[i]);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+    for (int q = 0; q < rounds; ++q) {
+      const int p = cb + q * SEL_ROUND + (warp * 32 + lane) * KPT;
+      if (!once) load(q);
+      if (!once || pass == 0) match = bit_range(m0 - p, min(m1, ce) - p);
+      if (pass > 0) {
+        uint32_t same = 0;
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) same |= (own[j] >> (shift + bits)) == prefix ? 1u << j : 0u;
+        match &= same;
+      }
+      if (pass == 0) {
+#pragma unroll
+        for (int j = 0; j < KPT; ++j)
+          if ((match >> j) & 1) atomicAdd(&hist[own[j] >> 21], 1);
+      } else {
+        for (uint32_t m = match; m; m &= m - 1) atomicAdd(&hist[(own[__ffs(m) - 1] >> shift) & mask], 1);
+      }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {  // largest bins first
-      int d = 255, left = need;
-      while (hist[d] < left) left -= hist[d--];
-      sh[0] = d;
-      sh[1] = left;
+    sm100::cluster_sync();
+    // bins from the largest down, two per thread: d and d - 1
+    const int d = SEL_BINS - 1 - 2 * threadIdx.x;
+    int2 part[SEL_CLUSTER], c = {0, 0};
+#pragma unroll
+    for (int r = 0; r < SEL_CLUSTER; ++r) part[r] = r < CL ? load_remote2(&hist[d - 1], r) : make_int2(0, 0);
+#pragma unroll
+    for (int r = 0; r < SEL_CLUSTER; ++r) {
+      c.x += part[r].x;
+      c.y += part[r].y;
     }
+    int before = warp_excl(c.x + c.y, lane);
+    if (lane == 31) sWarp[0][warp] = before + c.x + c.y;
     __syncthreads();
-    prefix = prefix << 8 | (uint32_t)sh[0];
-    need = sh[1];
-    __syncthreads();
+    before += __shfl_sync(0xffffffffu, warp_excl(sWarp[0][lane], lane), warp);
+    if (before < need && need <= before + c.x + c.y) {  // one thread
+      const bool second = need > before + c.y;
+      sPick[0] = second ? d - 1 : d;
+      sPick[1] = need - before - (second ? c.y : 0);
+    }
+    sm100::cluster_sync();  // (also: every CTA has read this one's counts)
+    prefix = prefix << bits | (uint32_t)sPick[0];
+    need = sPick[1];
   }
-  // prefix: the key of the last kept middle token; need: how many with exactly that key
-  const bool none = keep == first + recent;
-  int nkept = 0, nties = 0;
-  for (int base = 0; base < len; base += SEL_THREADS) {
-    const int i = base + threadIdx.x;
-    const bool in = i < len, mid = in && i >= m0 && i < m1;
-    const uint32_t k = mid ? weight_key(w[i]) : 0;
-    const bool tie = mid && !none && k == prefix;
-    const unsigned tb = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) wsum[0][warp] = __popc(tb);
-    __syncthreads();
-    int t = nties + __popc(tb & ((1u << lane) - 1)), tall = nties;
-    for (int x = 0; x < SEL_THREADS / 32; ++x) {
-      if (x < warp) t += wsum[0][x];
-      tall += wsum[0][x];
+  // prefix: the key of the last kept middle token; need: how many with exactly that key.  A lane's sure
+  // positions (forced, or above the key) and tied ones as bits, and their counts before it in its warp
+  auto bits_of = [&](int p, uint32_t& sure, uint32_t& tie) {
+    const uint32_t in = bit_range(0, ce - p), mid = bit_range(m0 - p, min(m1, ce) - p);
+    uint32_t above = 0, equal = 0;
+    if (!none) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) {
+        const uint32_t k = own[j];
+        above |= k > prefix ? 1u << j : 0u;
+        equal |= k == prefix ? 1u << j : 0u;
+      }
     }
-    const bool take = in && (!mid || (!none && k > prefix) || (tie && t < need));
-    const unsigned kb = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) wsum[1][warp] = __popc(kb);
-    __syncthreads();
-    int at = nkept + __popc(kb & ((1u << lane) - 1)), kall = nkept;
-    for (int x = 0; x < SEL_THREADS / 32; ++x) {
-      if (x < warp) at += wsum[1][x];
-      kall += wsum[1][x];
+    sure = in & (~mid | above);
+    tie = mid & equal;
+  };
+  int nkeep = 0, ntie = 0;
+  for (int q = 0; q < rounds; ++q) {
+    if (!once) load(q);
+    uint32_t su, ti;
+    bits_of(cb + q * SEL_ROUND + (warp * 32 + lane) * KPT, su, ti);
+    nkeep += __popc(su);
+    ntie += __popc(ti);
+  }
+  // (over all rounds of a CTA; with several rounds the warps' parts interleave and are ordered below)
+  nkeep = __reduce_add_sync(0xffffffffu, nkeep);
+  ntie = __reduce_add_sync(0xffffffffu, ntie);
+  if (lane == 0) {
+    sWarp[0][warp] = nkeep;
+    sWarp[1][warp] = ntie;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    nkeep = __reduce_add_sync(0xffffffffu, sWarp[0][lane]);
+    ntie = __reduce_add_sync(0xffffffffu, sWarp[1][lane]);
+    if (lane == 0) {
+      sTot[0] = nkeep;
+      sTot[1] = ntie;
     }
-    if (take && at < keep) {
-      out[at] = i;
-      if (w2) w2[at] = w[i];
-    }
-    nkept = kall;
-    nties = tall;
+  }
+  sm100::cluster_sync();
+  int kb = 0, tb = 0;  // sure ones and ties before the current round
+  for (int r = 0; r < rank; ++r) {
+    const int2 t = load_remote2(sTot, r);
+    kb += t.x;
+    tb += t.y;
+  }
+  sm100::cluster_sync();  // no CTA leaves while another reads its counts
+  for (int q = 0; q < rounds; ++q) {
+    const int p = cb + q * SEL_ROUND + (warp * 32 + lane) * KPT;
+    if (!once) load(q);
+    uint32_t su, ti;
+    bits_of(p, su, ti);
+    int k = warp_excl(__popc(su), lane), t = warp_excl(__popc(ti), lane);
     __syncthreads();
+    if (lane == 31) {
+      sWarp[0][warp] = k + __popc(su);
+      sWarp[1][warp] = t + __popc(ti);
+    }
+    __syncthreads();
+    const int a0 = sWarp[0][lane], a1 = sWarp[1][lane];
+    k += kb + __shfl_sync(0xffffffffu, warp_excl(a0, lane), warp);
+    t += tb + __shfl_sync(0xffffffffu, warp_excl(a1, lane), warp);
+    kb += __reduce_add_sync(0xffffffffu, a0);
+    tb += __reduce_add_sync(0xffffffffu, a1);
+    for (uint32_t m = su | ti; m; m &= m - 1) {
+      const int j = __ffs(m) - 1, i = p + j;
+      const bool tied = (ti >> j) & 1;
+      const int at = k + min(t, need);
+      if (!tied || t < need) {
+        if (at < keep) {
+          out[at] = i;
+          if (w2) w2[at] = w[i];
+        }
+      }
+      k += !tied;
+      t += tied;
+    }
   }
 }
 
 // Kept rows into the new cache, a token block at a time: one CTA per (block, K or V and head, sequence).
+// The largest magnitude is found on the codes themselves (their low 7 bits order like the values), a
+// chunk at a time with its own scale, and codes whose scale stays are copied as they are.
 template <int DH, int CH>
 __global__ void __launch_bounds__(256) compact_kernel(Kv8Args a, Kv8Args d, const int* kept, int keep, const int* lens2) {
   __shared__ float red[8];
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+  wait_previous_kernel();
   const int t0 = blockIdx.x * d.block, rows = min(d.block, lens2[b] - t0);
   if (rows <= 0) return;
   const size_t hd = (size_t)b * a.Hkv + g;
   const uint8_t* src = (const uint8_t*)(kv ? a.v : a.k) + hd * a.Lmax * DH;
   const float* ss = (kv ? a.vs : a.ks) + hd * a.nblk;
   uint8_t* dst = (uint8_t*)(kv ? d.v : d.k) + (hd * d.Lmax + t0) * DH;
-  float v[CH][16], m = 0.f;
+  int j[CH];
+  uint4 v[CH];
+  float sc[CH], m = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int ch = i * 256 + threadIdx.x;
-    if (ch < rows * CPR) {
-      const int j = kept[hd * keep + t0 + ch / CPR];
-      decode16(*(const uint4*)(src + (size_t)j * DH + ch % CPR * 16), ss[j / a.block], v[i]);
-      m = fmaxf(m, amax16(v[i]));
-    }
+    j[i] = ch < rows * CPR ? kept[hd * keep + t0 + ch / CPR] : -1;
   }
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (j[i] >= 0) {
+      v[i] = __ldg((const uint4*)(src + (size_t)j[i] * DH + (i * 256 + threadIdx.x) % CPR * 16));
+      sc[i] = __ldg(ss + (j[i] >> a.lb));
+    }
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (j[i] >= 0) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t x = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t y = w[k] & 0x7f7f7f7fu;
+        x = __vmaxu4(x, y & ~__vcmpeq4(y, 0x7f7f7f7fu));  // (NaN does not count)
+      }
+      x = __vmaxu4(x, x >> 16);
+      m = fmaxf(m, e4m3x2_to_f2(max(x & 0xff, (x >> 8) & 0xff)).x * sc[i]);
+    }
   m = block_max<256>(m, red);
   const int e = scale_exp(m);
-  const float inv = pow2(-e);
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int ch = i * 256 + threadIdx.x;
-    if (ch < rows * CPR) *(uint4*)(dst + (size_t)(ch / CPR) * DH + ch % CPR * 16) = encode16(v[i], inv);
-  }
+  for (int i = 0; i < CH; ++i)
+    if (j[i] >= 0) {
+      if (exp_of(sc[i]) != e) v[i] = rescale16(v[i], exp_of(sc[i]) - e);
+      *(uint4*)(dst + (size_t)(i * 256 + threadIdx.x) * 16) = v[i];
+    }
   if (threadIdx.x == 0) (kv ? d.vs : d.ks)[hd * d.nblk + blockIdx.x] = pow2(e);
 }
 
@@ -1076,16 +1251,33 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
 
 cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, int keep, int first, int recent,
                       const Kv8Args& d, int* lens2, float* weights2, int* kept, cudaStream_t s) {
-  kv8::select_kernel<<<a.B * a.Hkv, kv8::SEL_THREADS, 0, s>>>(weights, a.Lmax, a.Hkv, lens, keep, first, recent, kept, lens2,
-                                                             weights2, d.Lmax);
-  cudaError_t e = cudaGetLastError();
+  // CTAs per head: shares of 4096 positions, at most 8 (portable), and no more than about two CTAs per SM
+  // over all heads
+  int dev = 0, sms = 148, cl = 1;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  while (cl < kv8::SEL_CLUSTER && cl * 4096 < a.Lmax && cl * a.B * a.Hkv <= sms) cl *= 2;
+  cudaError_t e = cudaFuncSetAttribute(kv8::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kv8::SEL_SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cl;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(a.B * a.Hkv * cl);
+  lc.blockDim = dim3(kv8::SEL_THREADS);
+  lc.dynamicSmemBytes = kv8::SEL_SMEM;
+  lc.stream = s;
+  lc.attrs = &attr;
+  lc.numAttrs = 1;
+  e = cudaLaunchKernelEx(&lc, kv8::select_kernel, weights, a.Lmax, a.Hkv, cl, lens, keep, first, recent, kept, lens2,
+                         weights2, d.Lmax);
   if (e != cudaSuccess) return e;
   const dim3 grid((keep + d.block - 1) / d.block, 2 * a.Hkv, a.B);
   auto run = [&](auto dh) {
     constexpr int DH = decltype(dh)::value;
     return kv8::with_chunks(d.block, DH, [&](auto ch) {
-      kv8::compact_kernel<DH, decltype(ch)::value><<<grid, 256, 0, s>>>(a, d, kept, keep, lens2);
-      return cudaGetLastError();
+      return launch_dependent(kv8::compact_kernel<DH, decltype(ch)::value>, grid, 256, s, a, d, (const int*)kept, keep,
+                              (const int*)lens2);
     });
   };
   return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());

@@ -359,6 +359,35 @@ def test_evict(mka, L, lens, keep, first, recent, block, block2, kind):
     assert mka.mka_status() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,L,keep", [(2, 9000, 8000), (1, 20000, 1234), (1, 70001, 40000), (1, 262144, 300),
+                                      (1, 270000, 2000), (40, 9000, 60)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_long(mka, B, L, keep, ties):
+    """Several CTAs per head, keys in few and many registers and read again; the order over warps and CTAs."""
+    dh = 64
+    c, c2 = mka.make_kv8_config(B, L, 1, 1, dh), mka.make_kv8_config(B, keep, 1, 1, dh)
+    g = gen(L)
+    codes = [torch.randint(0, 0x7f, (B, 1, L, dh), generator=g, dtype=torch.uint8).cuda() for _ in range(2)]
+    sc = [torch.exp2(torch.randint(-3, 4, (B, 1, -(-L // 64)), generator=g) * 1.0).cuda() for _ in range(2)]
+    cache = mka.kv8_cache(*codes, *sc)
+    w = torch.rand(B, 1, L, generator=g)
+    if ties:
+        w = torch.randint(0, 2, (B, 1, L), generator=g) * 0.25 + (torch.rand(B, 1, L, generator=g) < keep / L / 3)
+    lens = [L - 37 * b for b in range(B)]
+    d, lens2, w2, kept = evict(mka, c, cache, lens, w, keep, 3, 20, c2)
+    assert lens2 == [keep] * B
+    got = read(mka, c2, d, lens2)
+    for b in range(B):
+        pick = torch.tensor(ref.keep_positions(w[b, 0].tolist(), lens[b], keep, 3, 20))
+        assert torch.equal(kept[b, 0].long(), pick) and torch.equal(w2[b, 0], w[b, 0, pick])
+        for kv in range(2):
+            x = codes[kv][b, 0].view(torch.float8_e4m3fn).cpu()[pick].double() * sc[kv][b, 0].cpu().double()[pick // 64, None]
+            m = ref.Cache(64)
+            m.append(0, x)
+            assert torch.equal(got[kv][b, :, 0], m.x)
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.gpu
 def test_prompt_decode_evict_decode(mka):
