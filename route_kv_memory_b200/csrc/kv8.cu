@@ -151,9 +151,9 @@ __device__ __forceinline__ float block_max(float v, float* s) {
 // ============================================================================ append
 // One block of threads per (touched token block, K or V and head, sequence).  The new rows of the token
 // block stay in registers between the maximum and the codes, so each is read once.
-constexpr int AP_THREADS = 256;
+constexpr int AP_THREADS = 128;
 
-template <typename T, int DH, int CH>  // CH: 16-value chunks per thread, CH * 256 >= block * DH / 16
+template <typename T, int DH, int CH>  // CH: 16-value chunks per thread, CH * AP_THREADS >= block * DH / 16
 __global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* kn, const T* vn, long long row_stride,
                                                             long long batch_stride, int n, const int* pos,
                                                             const int* count, int* status) {
@@ -201,27 +201,42 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* 
 }
 
 // ============================================================================ read
-// Thread per 16 codes; rows [first[b], first[b] + rows[b]) of sequence b to rows 0.. of the outputs.
-template <typename T, int DH>
+// Rows [first[b], first[b] + rows[b]) of sequence b to rows 0.. of the outputs; a block takes one head of K
+// or V, a thread NC chunks of 16 codes, 256 apart, with all their loads in flight.
+template <typename T, int DH, int NC>
 __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, const int* rows, int n, T* k_out,
                                                    T* v_out, long long row_stride, long long batch_stride, int* status) {
   constexpr int CPR = DH / 16;
-  const int b = blockIdx.z, kv = blockIdx.y;
+  const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
   const int f = first ? first[b] : 0, r = rows ? min(max(rows[b], 0), n) : n;
   if (f < 0 || (long long)f + r > a.Lmax) {
     if (threadIdx.x == 0) set_status(status, kStatusBounds);
     return;
   }
-  // (row, head, chunk), chunk fastest: a warp writes 32 chunks of consecutive output columns
-  const int at = blockIdx.x * 256 + threadIdx.x, per = a.Hkv * CPR;
-  const int row = at / per, g = at % per / CPR, ch = at % CPR;
-  if (row >= r) return;
   const size_t hd = (size_t)b * a.Hkv + g;
-  const uint8_t* codes = (const uint8_t*)(kv ? a.v : a.k) + (hd * a.Lmax + f + row) * DH + ch * 16;
-  const float s = (kv ? a.vs : a.ks)[hd * a.nblk + ((f + row) >> a.lb)];
-  float x[16];
-  decode16(*(const uint4*)codes, s, x);
-  store16<T>((kv ? v_out : k_out) + (size_t)b * batch_stride + (size_t)row * row_stride + g * DH + ch * 16, x);
+  const uint8_t* codes = (const uint8_t*)(kv ? a.v : a.k) + (hd * a.Lmax + f) * DH;
+  const float* sc = (kv ? a.vs : a.ks) + hd * a.nblk;
+  T* out = (kv ? v_out : k_out) + (size_t)b * batch_stride + g * DH;
+  const int at = blockIdx.x * (256 * NC) + threadIdx.x, ch = at % CPR;
+  uint4 v[NC];
+  float s[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int row = (at + i * 256) / CPR;
+    if (row < r) {
+      v[i] = __ldg((const uint4*)(codes + (size_t)row * DH + ch * 16));
+      s[i] = __ldg(sc + ((f + row) >> a.lb));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int row = (at + i * 256) / CPR;
+    if (row < r) {
+      float y[16];
+      decode16(v[i], s[i], y);
+      store16<T>(out + (size_t)row * row_stride + ch * 16, y);
+    }
+  }
 }
 
 // ============================================================================ attention
@@ -886,6 +901,10 @@ __device__ __forceinline__ int2 load_remote2(const int* p, uint32_t rank) {
                : "=r"(v.x), "=r"(v.y) : "r"(sm100::smem_u32(p)), "r"(rank) : "memory");
   return v;
 }
+__device__ __forceinline__ void store_remote2(int* p, uint32_t rank, int2 v) {
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tst.shared::cluster.v2.b32 [r], {%2, %3};\n\t}"
+               :: "r"(sm100::smem_u32(p)), "r"(rank), "r"(v.x), "r"(v.y) : "memory");
+}
 __device__ __forceinline__ int warp_excl(int v, int lane) {  // exclusive prefix sum over the lanes
   int x = v;
 #pragma unroll
@@ -904,23 +923,20 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
 }
 
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weights, int Lmax, int Hkv, int CL, const int* lens,
-                                                             int keep, int first, int recent, int* kept, int* lens2,
-                                                             float* weights2, int L2max) {
+                                                             int keep, int first, int recent, int* kept, int* lens2) {
   extern __shared__ uint32_t skeys[];
-  __shared__ __align__(8) int hist[SEL_BINS];
+  __shared__ __align__(8) int hist[SEL_BINS], all[SEL_BINS];  // this CTA's counts, the cluster's
   __shared__ __align__(8) int sTot[2];
   __shared__ int sWarp[2][SEL_WARPS], sPick[2];
   const int hd = blockIdx.x / CL, rank = blockIdx.x % CL, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int len = min(max(lens[b], 0), Lmax);
   const float* w = weights + (size_t)hd * Lmax;
   int* out = kept + (size_t)hd * keep;
-  float* w2 = weights2 ? weights2 + (size_t)hd * L2max : nullptr;
   allow_next_kernel();
   if (threadIdx.x == 0 && rank == 0 && hd % Hkv == 0) lens2[b] = min(len, keep);
   if (len <= keep) {  // all of a short sequence (every CTA of the cluster takes this way)
     for (int i = rank * SEL_THREADS + threadIdx.x; i < keep; i += CL * SEL_THREADS) {
       out[i] = i < len ? i : -1;
-      if (w2 && i < len) w2[i] = w[i];
     }
     return;
   }
@@ -973,17 +989,28 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
         for (uint32_t m = match; m; m &= m - 1) atomicAdd(&hist[(own[__ffs(m) - 1] >> shift) & mask], 1);
       }
     }
-    sm100::cluster_sync();
+    if (CL > 1) {
+      // every CTA adds up the counts of its slices of 256 bins, 8 lanes (a CTA's counts each) per pair of
+      // bins, and gives every CTA the sum
+      sm100::cluster_sync();
+      const int r = threadIdx.x % SEL_CLUSTER;
+      for (int sl = rank; sl < SEL_BINS / 256; sl += CL) {
+        int* bin = &hist[sl * 256 + threadIdx.x / SEL_CLUSTER * 2];
+        int2 c = r < CL ? load_remote2(bin, r) : make_int2(0, 0);
+#pragma unroll
+        for (int o = 1; o < SEL_CLUSTER; o <<= 1) {
+          c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
+          c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
+        }
+        if (r < CL) store_remote2(all + (bin - hist), r, c);
+      }
+      sm100::cluster_sync();  // (the next pass writes `all` only behind its own first barrier)
+    } else {
+      __syncthreads();
+    }
     // bins from the largest down, two per thread: d and d - 1
     const int d = SEL_BINS - 1 - 2 * threadIdx.x;
-    int2 part[SEL_CLUSTER], c = {0, 0};
-#pragma unroll
-    for (int r = 0; r < SEL_CLUSTER; ++r) part[r] = r < CL ? load_remote2(&hist[d - 1], r) : make_int2(0, 0);
-#pragma unroll
-    for (int r = 0; r < SEL_CLUSTER; ++r) {
-      c.x += part[r].x;
-      c.y += part[r].y;
-    }
+    const int2 c = *(const int2*)&(CL > 1 ? all : hist)[d - 1];
     int before = warp_excl(c.x + c.y, lane);
     if (lane == 31) sWarp[0][warp] = before + c.x + c.y;
     __syncthreads();
@@ -993,7 +1020,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
       sPick[0] = second ? d - 1 : d;
       sPick[1] = need - before - (second ? c.y : 0);
     }
-    sm100::cluster_sync();  // (also: every CTA has read this one's counts)
+    __syncthreads();
     prefix = prefix << bits | (uint32_t)sPick[0];
     need = sPick[1];
   }
@@ -1014,9 +1041,9 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
     tie = mid & equal;
   };
   int nkeep = 0, ntie = 0;
+  uint32_t su = 0, ti = 0;
   for (int q = 0; q < rounds; ++q) {
     if (!once) load(q);
-    uint32_t su, ti;
     bits_of(cb + q * SEL_ROUND + (warp * 32 + lane) * KPT, su, ti);
     nkeep += __popc(su);
     ntie += __popc(ti);
@@ -1039,17 +1066,21 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
   }
   sm100::cluster_sync();
   int kb = 0, tb = 0;  // sure ones and ties before the current round
-  for (int r = 0; r < rank; ++r) {
-    const int2 t = load_remote2(sTot, r);
-    kb += t.x;
-    tb += t.y;
+  int2 tot[SEL_CLUSTER];
+#pragma unroll
+  for (int r = 0; r < SEL_CLUSTER; ++r) tot[r] = r < rank ? load_remote2(sTot, r) : make_int2(0, 0);
+#pragma unroll
+  for (int r = 0; r < SEL_CLUSTER; ++r) {
+    kb += tot[r].x;
+    tb += tot[r].y;
   }
   sm100::cluster_sync();  // no CTA leaves while another reads its counts
   for (int q = 0; q < rounds; ++q) {
     const int p = cb + q * SEL_ROUND + (warp * 32 + lane) * KPT;
-    if (!once) load(q);
-    uint32_t su, ti;
-    bits_of(p, su, ti);
+    if (!once) {
+      load(q);
+      bits_of(p, su, ti);
+    }
     int k = warp_excl(__popc(su), lane), t = warp_excl(__popc(ti), lane);
     __syncthreads();
     if (lane == 31) {
@@ -1066,12 +1097,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
       const int j = __ffs(m) - 1, i = p + j;
       const bool tied = (ti >> j) & 1;
       const int at = k + min(t, need);
-      if (!tied || t < need) {
-        if (at < keep) {
-          out[at] = i;
-          if (w2) w2[at] = w[i];
-        }
-      }
+      if ((!tied || t < need) && at < keep) out[at] = i;
       k += !tied;
       t += tied;
     }
@@ -1082,8 +1108,9 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
 // The largest magnitude is found on the codes themselves (their low 7 bits order like the values), a
 // chunk at a time with its own scale, and codes whose scale stays are copied as they are.
 template <int DH, int CH>
-__global__ void __launch_bounds__(256) compact_kernel(Kv8Args a, Kv8Args d, const int* kept, int keep, const int* lens2) {
-  __shared__ float red[8];
+__global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args d, const int* kept, int keep, const int* lens2,
+                                                      const float* weights, float* weights2) {
+  __shared__ float red[AP_THREADS / 32];
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
   wait_previous_kernel();
@@ -1093,18 +1120,20 @@ __global__ void __launch_bounds__(256) compact_kernel(Kv8Args a, Kv8Args d, cons
   const uint8_t* src = (const uint8_t*)(kv ? a.v : a.k) + hd * a.Lmax * DH;
   const float* ss = (kv ? a.vs : a.ks) + hd * a.nblk;
   uint8_t* dst = (uint8_t*)(kv ? d.v : d.k) + (hd * d.Lmax + t0) * DH;
+  if (!kv && weights2 && threadIdx.x < rows)
+    weights2[hd * d.Lmax + t0 + threadIdx.x] = weights[hd * a.Lmax + kept[hd * keep + t0 + threadIdx.x]];
   int j[CH];
   uint4 v[CH];
   float sc[CH], m = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int ch = i * 256 + threadIdx.x;
+    const int ch = i * AP_THREADS + threadIdx.x;
     j[i] = ch < rows * CPR ? kept[hd * keep + t0 + ch / CPR] : -1;
   }
 #pragma unroll
   for (int i = 0; i < CH; ++i)
     if (j[i] >= 0) {
-      v[i] = __ldg((const uint4*)(src + (size_t)j[i] * DH + (i * 256 + threadIdx.x) % CPR * 16));
+      v[i] = __ldg((const uint4*)(src + (size_t)j[i] * DH + (i * AP_THREADS + threadIdx.x) % CPR * 16));
       sc[i] = __ldg(ss + (j[i] >> a.lb));
     }
 #pragma unroll
@@ -1120,24 +1149,25 @@ __global__ void __launch_bounds__(256) compact_kernel(Kv8Args a, Kv8Args d, cons
       x = __vmaxu4(x, x >> 16);
       m = fmaxf(m, e4m3x2_to_f2(max(x & 0xff, (x >> 8) & 0xff)).x * sc[i]);
     }
-  m = block_max<256>(m, red);
+  m = block_max<AP_THREADS>(m, red);
   const int e = scale_exp(m);
 #pragma unroll
   for (int i = 0; i < CH; ++i)
     if (j[i] >= 0) {
       if (exp_of(sc[i]) != e) v[i] = rescale16(v[i], exp_of(sc[i]) - e);
-      *(uint4*)(dst + (size_t)(i * 256 + threadIdx.x) * 16) = v[i];
+      *(uint4*)(dst + (size_t)(i * AP_THREADS + threadIdx.x) * 16) = v[i];
     }
   if (threadIdx.x == 0) (kv ? d.vs : d.ks)[hd * d.nblk + blockIdx.x] = pow2(e);
 }
 
-// Calls f(integral_constant) with the 16-value chunks per thread of a token block of 256 threads.
+// Calls f(integral_constant) with the 16-value chunks per thread of a token block.
 template <typename F>
 cudaError_t with_chunks(int block, int dh, F f) {
-  const int ch = (block * dh / 16 + 255) / 256;
+  const int ch = (block * dh / 16 + AP_THREADS - 1) / AP_THREADS;
   if (ch <= 1) return f(std::integral_constant<int, 1>());
   if (ch <= 2) return f(std::integral_constant<int, 2>());
-  return f(std::integral_constant<int, 4>());
+  if (ch <= 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, 8>());
 }
 
 }  // namespace kv8
@@ -1163,19 +1193,24 @@ cudaError_t kv8_append(const Kv8Args& a, const void* kn, const void* vn, int is_
 
 cudaError_t kv8_read(const Kv8Args& a, const int* first, const int* rows, int n, void* k_out, void* v_out, int is_bf16,
                      long long row_stride, long long batch_stride, int* status, cudaStream_t s) {
-  const long long chunks = (long long)n * a.Hkv * (a.dh / 16);
-  const dim3 grid((unsigned)((chunks + 255) / 256), 2, a.B);
-  auto run = [&](auto dh) {
-    constexpr int DH = decltype(dh)::value;
-    if (is_bf16)
-      kv8::read_kernel<bf16, DH><<<grid, 256, 0, s>>>(a, first, rows, n, (bf16*)k_out, (bf16*)v_out, row_stride,
-                                                      batch_stride, status);
-    else
-      kv8::read_kernel<float, DH><<<grid, 256, 0, s>>>(a, first, rows, n, (float*)k_out, (float*)v_out, row_stride,
-                                                       batch_stride, status);
+  const int chunks = n * (a.dh / 16);  // of one head
+  auto run = [&](auto type, auto dh, auto nc) {
+    using T = decltype(type);
+    constexpr int NC = decltype(nc)::value;
+    const dim3 grid((chunks + 256 * NC - 1) / (256 * NC), 2 * a.Hkv, a.B);
+    kv8::read_kernel<T, decltype(dh)::value, NC><<<grid, 256, 0, s>>>(a, first, rows, n, (T*)k_out, (T*)v_out, row_stride,
+                                                                      batch_stride, status);
     return cudaGetLastError();
   };
-  return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
+  // two chunks a thread once that still leaves every SM four blocks; fewer rows: more threads
+  auto with_nc = [&](auto type, auto dh) {
+    return (long long)chunks * 2 * a.Hkv * a.B >= 2 * 256 * 148 * 4 ? run(type, dh, std::integral_constant<int, 2>())
+                                                                    : run(type, dh, std::integral_constant<int, 1>());
+  };
+  auto with_dh = [&](auto type) {
+    return a.dh == 128 ? with_nc(type, std::integral_constant<int, 128>()) : with_nc(type, std::integral_constant<int, 64>());
+  };
+  return is_bf16 ? with_dh(bf16()) : with_dh(float());
 }
 
 // Groups of 8 query rows per unit: a second one shares the cache's bytes and conversions.
@@ -1269,15 +1304,14 @@ cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, i
   lc.stream = s;
   lc.attrs = &attr;
   lc.numAttrs = 1;
-  e = cudaLaunchKernelEx(&lc, kv8::select_kernel, weights, a.Lmax, a.Hkv, cl, lens, keep, first, recent, kept, lens2,
-                         weights2, d.Lmax);
+  e = cudaLaunchKernelEx(&lc, kv8::select_kernel, weights, a.Lmax, a.Hkv, cl, lens, keep, first, recent, kept, lens2);
   if (e != cudaSuccess) return e;
   const dim3 grid((keep + d.block - 1) / d.block, 2 * a.Hkv, a.B);
   auto run = [&](auto dh) {
     constexpr int DH = decltype(dh)::value;
     return kv8::with_chunks(d.block, DH, [&](auto ch) {
-      return launch_dependent(kv8::compact_kernel<DH, decltype(ch)::value>, grid, 256, s, a, d, (const int*)kept, keep,
-                              (const int*)lens2);
+      return launch_dependent(kv8::compact_kernel<DH, decltype(ch)::value>, grid, kv8::AP_THREADS, s, a, d, (const int*)kept, keep,
+                              (const int*)lens2, weights, weights2);
     });
   };
   return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
