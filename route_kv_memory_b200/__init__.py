@@ -9,6 +9,7 @@ load, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -268,17 +269,22 @@ def _dtype(t: torch.Tensor, want: torch.dtype, name: str) -> None:
         raise ValueError(f"{name} must be {want}, not {t.dtype}")
 
 
-def _call_stream(tensors, stream):
-    """The stream pointer of a call on `tensors`: they must live on the current device, and a stream
-    other than the current one is recorded on them."""
+def _call_stream(tensors, stream, *caches):
+    """The stream pointer of a call on `tensors` (and 8-bit caches): they must live on the current device, and
+    a stream other than the current one is recorded on them."""
     dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"every tensor of the call must live on the current CUDA device ({dev})")
+    for x in caches:
+        if x.tensors[0].get_device() != dev:  # (its tensors share a device)
+            raise ValueError(f"the cache must live on the current CUDA device ({dev})")
     current = torch._C._cuda_getCurrentRawStream(dev)  # (a Stream object per call would cost microseconds)
     if stream is None:
         return current
     if stream.cuda_stream != current:
+        for x in caches:
+            tensors = (*tensors, *x.tensors)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -289,12 +295,8 @@ def _dense(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, *shape: int
     """Pointer of a contiguous tensor of that type and number of elements (None passes)."""
     if t is None:
         return None
-    _dtype(t, dtype, name)
-    n = 1
-    for s in shape:
-        n *= s
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {shape} elements, not {tuple(t.shape)}")
+    if t.dtype != dtype or t.numel() != math.prod(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} with {shape} elements, not {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -378,40 +380,49 @@ def kv8_cache(k, v, k_scale, v_scale) -> mka_kv8_cache:
         raise ValueError("codes must be [B, Hkv, max_positions, dh] of float8_e4m3fn or uint8")
     if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != v_scale.shape or k_scale.dim() != 3:
         raise ValueError("scales must be [B, Hkv, blocks] of float32")
+    if not k.get_device() == v.get_device() == k_scale.get_device() == v_scale.get_device():
+        raise ValueError("the tensors of an 8-bit cache must live on one device")
     x = mka_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
     x.tensors = (k, v, k_scale, v_scale)
+    x.shapes = (*k.shape, *k_scale.shape)
     return x
 
 
 def _check_cache(c: mka_kv8_config, x: mka_kv8_cache) -> None:
-    k, _, s, _ = x.tensors
-    if k.shape != (c.batch, c.n_kv_heads, c.max_positions, c.d_head):
-        raise ValueError(f"the cache's codes are {tuple(k.shape)}, not what the configuration says")
-    if c.block > 0 and s.shape != (c.batch, c.n_kv_heads, -(-c.max_positions // c.block)):
-        raise ValueError(f"the cache's scales are {tuple(s.shape)}, not what the configuration says")
+    B, H, L, blk = c.batch, c.n_kv_heads, c.max_positions, c.block
+    if x.shapes != (B, H, L, c.d_head, B, H, -(-L // blk) if blk > 0 else 0):
+        raise ValueError(f"the cache's codes and scales are {x.shapes[:4]}, {x.shapes[4:]}, not what the configuration says")
 
 
 def _kv_rows(c: mka_kv8_config, t: torch.Tensor, name: str):
     """(rows, row stride, batch stride) of K/V rows [B, n, Hkv, dh] or [B, n, Hkv * dh]."""
     _dtype(t, torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32, name)
-    width = c.n_kv_heads * c.d_head
-    n = t.shape[1] if t.dim() in (3, 4) else -1
-    if t.shape not in ((c.batch, n, c.n_kv_heads, c.d_head), (c.batch, n, width)):
-        raise ValueError(f"{name} must be [{c.batch}, n, {c.n_kv_heads}, {c.d_head}], not {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 or (t.dim() == 4 and c.n_kv_heads > 1 and st[2] != c.d_head):
+    B, H, d, shape, st = c.batch, c.n_kv_heads, c.d_head, t.shape, t.stride()
+    n = shape[1] if len(shape) > 2 else -1
+    if shape == (B, n, H, d):
+        packed = st[3] == 1 and (H == 1 or st[2] == d)
+    elif shape == (B, n, H * d):
+        packed = st[2] == 1
+    else:
+        raise ValueError(f"{name} must be [{B}, n, {H}, {d}], not {tuple(shape)}")
+    if not packed:
         raise ValueError(f"{name}: the elements of a row must be contiguous, strides {st}")
-    return n, (st[1] if n > 1 else width), (st[0] if c.batch > 1 else 0)
+    return n, (st[1] if n > 1 else H * d), (st[0] if B > 1 else 0)
+
+
+def _kv_pair(c: mka_kv8_config, k: torch.Tensor, v: torch.Tensor, names: str):
+    rows = _kv_rows(c, k, names[0])
+    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError(f"{names[0]} and {names[1]} must have the same type, shape and strides")
+    return rows
 
 
 def mka_kv8_append(c: mka_kv8_config, cache: mka_kv8_cache, k_new, v_new, pos, count=None, stream=None) -> None:
     """k_new, v_new [B, n, Hkv, dh] of the configuration's type (row and batch strides allowed, the same for both);
     pos, count [B] int32 on the device."""
-    s = _call_stream((k_new, v_new, pos, count) + cache.tensors, stream)
+    s = _call_stream((k_new, v_new, pos, count), stream, cache)
     _check_cache(c, cache)
-    rows = _kv_rows(c, k_new, "k_new")
-    if _kv_rows(c, v_new, "v_new") != rows:
-        raise ValueError("k_new and v_new must have the same shape and strides")
+    rows = _kv_pair(c, k_new, v_new, ("k_new", "v_new"))
     _check(_lib.mka_kv8_append(c, cache, k_new.data_ptr(), v_new.data_ptr(), rows[1], rows[2], rows[0],
                                _dense(pos, "pos", torch.int32, c.batch), _dense(count, "count", torch.int32, c.batch), s),
            "mka_kv8_append")
@@ -419,11 +430,9 @@ def mka_kv8_append(c: mka_kv8_config, cache: mka_kv8_cache, k_new, v_new, pos, c
 
 def mka_kv8_read(c: mka_kv8_config, cache: mka_kv8_cache, first, rows, k_out, v_out, stream=None) -> None:
     """Values of positions first[b] .. first[b] + rows[b] - 1 to k_out, v_out [B, n, Hkv, dh] (strides allowed)."""
-    s = _call_stream((first, rows, k_out, v_out) + cache.tensors, stream)
+    s = _call_stream((first, rows, k_out, v_out), stream, cache)
     _check_cache(c, cache)
-    at = _kv_rows(c, k_out, "k_out")
-    if _kv_rows(c, v_out, "v_out") != at:
-        raise ValueError("k_out and v_out must have the same shape and strides")
+    at = _kv_pair(c, k_out, v_out, ("k_out", "v_out"))
     _check(_lib.mka_kv8_read(c, cache, _dense(first, "first", torch.int32, c.batch),
                              _dense(rows, "rows", torch.int32, c.batch), at[0], k_out.data_ptr(), v_out.data_ptr(), at[1],
                              at[2], s), "mka_kv8_read")
@@ -436,7 +445,7 @@ def mka_kv8_attention_workspace_size(c: mka_kv8_config, n: int = 1, with_weights
 def mka_kv8_attention(c: mka_kv8_config, cache: mka_kv8_cache, q, lens, out, weights, ws, stream=None) -> None:
     """Attention of the last n positions: q, out [B, n, Hq, dh] (or flat heads), dense; lens [B] int32 on the device;
     weights [B, Hkv, max_positions] float32 or None."""
-    s = _call_stream((q, lens, out, weights, ws) + cache.tensors, stream)
+    s = _call_stream((q, lens, out, weights, ws), stream, cache)
     _check_cache(c, cache)
     dt = torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32
     n = q.shape[1] if q.dim() >= 2 else 0
@@ -454,7 +463,7 @@ def mka_kv8_evict_workspace_size(c: mka_kv8_config, keep: int) -> int:
 def mka_kv8_evict(c: mka_kv8_config, cache: mka_kv8_cache, lens, weights, keep: int, first: int, recent: int,
                   dst_c: mka_kv8_config, dst: mka_kv8_cache, dst_lens, dst_weights, kept, ws, stream=None) -> None:
     """Keeps `keep` positions of every sequence and KV head (the first, the last, the heaviest) in another cache."""
-    s = _call_stream((lens, weights, dst_lens, dst_weights, kept, ws) + cache.tensors + dst.tensors, stream)
+    s = _call_stream((lens, weights, dst_lens, dst_weights, kept, ws), stream, cache, dst)
     _check_cache(c, cache)
     _check_cache(dst_c, dst)
     B, H = c.batch, c.n_kv_heads

@@ -746,30 +746,24 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
   if (threadIdx.x == 0) linger_after_abort(abort);  // a wait ran out: this CTA's copies land first
 }
 
-// Joins the partial results of one query row of one unit; a unit without tiles gives 0.  One CTA of eight
-// warps per (unit, row): the records' maxima first, then every warp adds a share of the records.
+// Joins the partial results of the query rows; a unit without tiles gives 0.  WPR warps per row: 8 (a CTA
+// per row) where a unit lies over many CTAs' ranges, 1 (8 rows a CTA) where it lies over a few.
 constexpr int MG_THREADS = 256;
-constexpr int MG_MOST = 1024;  // records of a unit = CTAs of the attention at most
-template <typename T, int DH, bool WT>
+constexpr int MG_MOST = 1024;  // CTAs of the attention at most
+template <typename T, int DH, bool WT, int WPR>
 __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, int grid) {
   using sm100::ex2;
   constexpr int PER = DH / 32;  // channels per lane
-  __shared__ long long sCount[MG_THREADS / 32][2];
-  __shared__ float sMax[MG_THREADS / 32][2], sSum[MG_THREADS / 32];
-  __shared__ float sFac[MG_MOST];
-  __shared__ float sX[MG_THREADS / 32][DH];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int NW = MG_THREADS / 32;
+  __shared__ long long sCount[NW][2];
+  __shared__ float sStat[NW][3], sX[NW][DH];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
   const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg;
-  const int row = blockIdx.x, g = blockIdx.y, b = blockIdx.z, rg = row / RT, r = row % RT, u = g * nrg + rg;
+  const int row = blockIdx.x * (NW / WPR) + warp / WPR, g = blockIdx.y, b = blockIdx.z, rg = row / RT, r = row % RT;
+  const int u = g * nrg + rg;
   const size_t hd = (size_t)b * a.c.Hkv + g;
-  T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) + (size_t)(g * a.G + row % a.G) * DH;
   allow_next_kernel();
   const Tiles ts = unit_tiles(a, b);
-  if (ts.n == 0) {
-    wait_previous_kernel();
-    if (threadIdx.x < DH) out[threadIdx.x] = from_f<T>(0.f);
-    return;
-  }
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < a.c.B; i += MG_THREADS) {
     const long long t = (long long)unit_tiles(a, i).n * upb;
@@ -785,70 +779,82 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
   __syncthreads();
   before = total = 0;
 #pragma unroll
-  for (int i = 0; i < MG_THREADS / 32; ++i) {
+  for (int i = 0; i < NW; ++i) {
     before += sCount[i][0];
     total += sCount[i][1];
   }
-  const long long share = (total + grid - 1) / grid, start = before + (long long)u * ts.n, end = start + ts.n - 1;
-  const int c0 = (int)(start / share), nrec = (int)(end / share) - c0 + 1;
   // every CTA waits, so that this kernel's end means the attention's too
   wait_previous_kernel();
-  if (nrec == 1) return;  // written whole by its CTA
-  const float* rec0 = a.part + (((size_t)b * upb + u + c0) * RT + r) * (DH + 4);
-  const size_t step = (size_t)RT * (DH + 4);
-  float L = -INFINITY, U = -INFINITY;
-  for (int i = threadIdx.x; i < nrec; i += MG_THREADS) {
-    const float4 h = *(const float4*)(rec0 + i * step);
-    L = fmaxf(L, h.x);
-    U = fmaxf(U, h.z);
-  }
-  L = warp_max(L);
-  U = warp_max(U);
-  if (lane == 0) {
-    sMax[warp][0] = L;
-    sMax[warp][1] = U;
-  }
-  __syncthreads();
+  if (row >= R) return;  // (WPR 8: never; WPR 1: no barrier follows)
+  T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) + (size_t)(g * a.G + row % a.G) * DH +
+           lane * PER;
+  if (ts.n == 0) {
 #pragma unroll
-  for (int i = 0; i < MG_THREADS / 32; ++i) {
-    L = fmaxf(L, sMax[i][0]);
-    U = fmaxf(U, sMax[i][1]);
+    for (int k = 0; k < PER; ++k) out[k] = from_f<T>(0.f);
+    return;
   }
-  float sum = 0.f;
-  for (int i = threadIdx.x; i < nrec; i += MG_THREADS) {
-    const float4 h = *(const float4*)(rec0 + i * step);
-    sum += h.x == -INFINITY ? h.y : h.y * ex2(h.x - L);
-    sFac[i] = h.z == -INFINITY ? 1.f : ex2(h.z - U);
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) sSum[warp] = sum;
-  __syncthreads();
-  float x[PER] = {};
-  for (int i = warp; i < nrec; i += MG_THREADS / 32) {
-    const float f = sFac[i];
-    const float* p = rec0 + i * step + 4 + lane * PER;
-    if constexpr (PER == 4) {
-      const float4 y = *(const float4*)p;
-      x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
-    } else {
-      const float2 y = *(const float2*)p;
-      x[0] += y.x * f; x[1] += y.y * f;
+  const long long share = (total + grid - 1) / grid, start = before + (long long)u * ts.n, end = start + ts.n - 1;
+  const int c0 = (int)(start / share), nrec = (int)(end / share) - c0 + 1;
+  if (nrec == 1) return;  // written whole by its CTA
+  const size_t step = (size_t)RT * (DH + 4);
+  const float* rec0 = a.part + (((size_t)b * upb + u + c0) * RT + r) * (DH + 4);
+  // this warp's records sub, sub + WPR, ..: 32 at a time, a lane's header each
+  float L = -INFINITY, U = -INFINITY, sum = 0.f, x[PER] = {};
+  for (int base = sub; base < nrec; base += 32 * WPR) {
+    const int i = base + lane * WPR;
+    const float4 h = i < nrec ? *(const float4*)(rec0 + i * step) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    const float nl = fmaxf(L, warp_max(h.x)), nu = fmaxf(U, warp_max(h.z));
+    const float fl = L == -INFINITY ? 1.f : ex2(L - nl), fu = U == -INFINITY ? 1.f : ex2(U - nu);
+    L = nl;
+    U = nu;
+    sum = sum * fl + warp_sum(h.x == -INFINITY ? h.y : h.y * ex2(h.x - L));
+#pragma unroll
+    for (int k = 0; k < PER; ++k) x[k] *= fu;
+    const float f = h.z == -INFINITY ? 1.f : ex2(h.z - U);
+    const int m = min(32, (nrec - base + WPR - 1) / WPR);
+#pragma unroll 4
+    for (int k = 0; k < m; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float* p = rec0 + (size_t)(base + k * WPR) * step + 4 + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 y = *(const float4*)p;
+        x[0] += y.x * fk; x[1] += y.y * fk; x[2] += y.z * fk; x[3] += y.w * fk;
+      } else {
+        const float2 y = *(const float2*)p;
+        x[0] += y.x * fk; x[1] += y.y * fk;
+      }
     }
   }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      sStat[warp][0] = L;
+      sStat[warp][1] = sum;
+      sStat[warp][2] = U;
+    }
 #pragma unroll
-  for (int k = 0; k < PER; ++k) sX[warp][lane * PER + k] = x[k];
-  __syncthreads();
-  if (threadIdx.x < DH) {
-    float v = 0.f;
+    for (int k = 0; k < PER; ++k) sX[warp][lane * PER + k] = x[k];
+    __syncthreads();
+    if (warp != 0) return;
     sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < MG_THREADS / 32; ++i) {
-      v += sX[i][threadIdx.x];
-      sum += sSum[i];
+    for (int i = 0; i < NW; ++i) {
+      L = fmaxf(L, sStat[i][0]);
+      U = fmaxf(U, sStat[i][2]);
     }
-    out[threadIdx.x] = from_f<T>(sum == 0.f ? 0.f : v * (ex2(U - L) / sum));
-    if (WT && threadIdx.x == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) x[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      sum += sStat[i][0] == -INFINITY ? sStat[i][1] : sStat[i][1] * ex2(sStat[i][0] - L);
+      const float f = sStat[i][2] == -INFINITY ? 1.f : ex2(sStat[i][2] - U);
+#pragma unroll
+      for (int k = 0; k < PER; ++k) x[k] += sX[i][lane * PER + k] * f;
+    }
   }
+  const float f = sum == 0.f ? 0.f : ex2(U - L) / sum;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) out[k] = from_f<T>(x[k] * f);
+  if (WT && lane == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
 }
 
 // weights[b][g][j] += sum over the query rows of KV head g of their softmax weight of token j, from the
@@ -1266,7 +1272,10 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
     if (e != cudaSuccess) return e;
     kernel<<<grid, kv8::AT_THREADS, smem, s>>>(tk, tv, a, status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_dependent(kv8::merge_kernel<T, DH, WT>, dim3(R, a.c.Hkv, a.c.B), kv8::MG_THREADS, s, a, 8 * NT, grid);
+    // few ranges per unit: a warp per row
+    const bool few = grid <= 8LL * a.c.B * a.c.Hkv * ((R + 8 * NT - 1) / (8 * NT));
+    e = launch_dependent(few ? kv8::merge_kernel<T, DH, WT, 1> : kv8::merge_kernel<T, DH, WT, 8>,
+                         dim3(few ? (R + 7) / 8 : R, a.c.Hkv, a.c.B), kv8::MG_THREADS, s, a, 8 * NT, grid);
     if (e != cudaSuccess || !WT) return e;
     return launch_dependent(kv8::weights_kernel, dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, s, a);
   };
