@@ -110,6 +110,29 @@ __device__ __forceinline__ void route_gate(float z0, float z1, float z2, int mod
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// Programmatic dependent launch.  A kernel launched by launch_dependent may start before the kernel in
+// front of it in the stream has finished, as soon as all of that one's CTAs have called
+// allow_next_kernel() or left.  It calls wait_previous_kernel(), which returns when the kernel in front
+// has finished and its writes are visible, before it touches memory that others may use, and in every
+// CTA, so that its own end means that everything in front has ended too.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Raise a kernel's dynamic shared memory limit.  Skipped while `s` is being
 // captured into a CUDA graph: the attribute persists, and an eager call made
 // before the capture has already set it.

@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* 
   __shared__ float red[AP_THREADS / 32];
   constexpr int CPR = DH / 16;  // chunks per row
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+  wait_previous_kernel();
+  allow_next_kernel();
   const int p = pos[b], c = count ? min(max(count[b], 0), n) : n;
   if (p < 0 || (long long)p + c > a.Lmax) {  // the whole sequence is left as it was
     if (threadIdx.x == 0) set_status(status, p < 0 ? kStatusBounds : kStatusCapacity);
@@ -208,6 +210,8 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
                                                    T* v_out, long long row_stride, long long batch_stride, int* status) {
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
+  wait_previous_kernel();
+  allow_next_kernel();
   const int f = first ? first[b] : 0, r = rows ? min(max(rows[b], 0), n) : n;
   if (f < 0 || (long long)f + r > a.Lmax) {
     if (threadIdx.x == 0) set_status(status, kStatusBounds);
@@ -300,10 +304,6 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t u) { return __half22float2(*(const __half2*)&u); }
 
-// Dependent launch: the next kernel of the stream may start its prologue; wait for the one before.
-__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Token (0..7) of row x (0..7) of an 8-row half of a S^T tile = contraction index x of O^T.  d_head 128
 // (128-byte rows, 16-byte chunk c of row t at chunk c ^ t): rows x and x ^ 1 differ in bit 2, so that
 // their K chunks 0-3 (4-7) land in different halves, and rows 0, 2, 4, 6 (1, 3, 5, 7) differ in bits 1-2,
@@ -348,13 +348,14 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
   uint8_t* mine = smem + warp * C::WARP;
   uint64_t* full = bars[warp];
 
-  allow_next_kernel();
   if (threadIdx.x == 0) {
     sAbort = 0;
     for (int i = 0; i < 4; ++i)
       for (int k = 0; k < STAGES; ++k) mbar_init(&bars[i][k], 1);
     fence_barrier_init();
   }
+  wait_previous_kernel();
+  allow_next_kernel();  // (not before: merge_kernel reads lens ahead of its own wait)
   // this CTA's range of tiles [w0, w1) and the sequence that w0 falls into
   long long total;
   {
@@ -484,17 +485,22 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
         for (int i = 0; i < 4; ++i) o[m][t][i] = 0.f;
     auto sees = [&](int j, int p) { return j <= p && (!a.window || j > p - a.window || j < a.sinks); };
 
+    float nks[2], nvs[2];  // the scales of the next tile's two halves, loaded a tile ahead
+    auto load_scales = [&](int it) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tb = min((ts.tile(first + it) * TILE + warp * 32 + 16 * h) >> a.c.lb, a.c.nblk - 1);
+        nks[h] = __ldg(ksc + tb);
+        nvs[h] = __ldg(vsc + tb);
+      }
+    };
+    load_scales(0);
     for (int it = 0; it < cnt; ++it, ++kvit) {
       const int st = kvit % STAGES, j0 = ts.tile(first + it) * TILE + warp * 32;
       const uint8_t* sk = mine + st * 2 * C::HALF;
       const uint8_t* sv = sk + C::HALF;
-      float kf[2], ev[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tb = min((j0 + 16 * h) >> a.c.lb, a.c.nblk - 1);
-        kf[h] = __ldg(ksc + tb);
-        ev[h] = (float)exp_of(__ldg(vsc + tb));
-      }
+      const float kf[2] = {nks[0], nks[1]}, ev[2] = {(float)exp_of(nvs[0]), (float)exp_of(nvs[1])};
+      if (it + 1 < cnt) load_scales(it + 1);
       if (!mbar_wait_warp(&full[st], (kvit / STAGES) & 1, abort, status)) break;
       // S^T of 32 tokens
       float s[2][NT][4];
@@ -763,7 +769,7 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
   const int u = g * nrg + rg;
   const size_t hd = (size_t)b * a.c.Hkv + g;
   allow_next_kernel();
-  const Tiles ts = unit_tiles(a, b);
+  const Tiles ts = unit_tiles(a, b);  // (lens is older than the attention, which waited before it started)
   long long before = 0, total = 0;
   for (int i = threadIdx.x; i < a.c.B; i += MG_THREADS) {
     const long long t = (long long)unit_tiles(a, i).n * upb;
@@ -861,8 +867,9 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
 // raw scores (log2 units) and each row's maximum and sum.  Thread per token of the unit's tiles.
 __global__ void __launch_bounds__(128) weights_kernel(Kv8Attn a) {
   const int b = blockIdx.z, g = blockIdx.y;
-  const Tiles ts = unit_tiles(a, b);
   wait_previous_kernel();
+  allow_next_kernel();
+  const Tiles ts = unit_tiles(a, b);
   if (blockIdx.x >= ts.n) return;
   const int j = ts.tile(blockIdx.x) * TILE + threadIdx.x, R = a.G * a.n;
   if (j >= ts.len) return;
@@ -935,10 +942,11 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
   __shared__ __align__(8) int sTot[2];
   __shared__ int sWarp[2][SEL_WARPS], sPick[2];
   const int hd = blockIdx.x / CL, rank = blockIdx.x % CL, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_previous_kernel();
+  allow_next_kernel();
   const int len = min(max(lens[b], 0), Lmax);
   const float* w = weights + (size_t)hd * Lmax;
   int* out = kept + (size_t)hd * keep;
-  allow_next_kernel();
   if (threadIdx.x == 0 && rank == 0 && hd % Hkv == 0) lens2[b] = min(len, keep);
   if (len <= keep) {  // all of a short sequence (every CTA of the cluster takes this way)
     for (int i = rank * SEL_THREADS + threadIdx.x; i < keep; i += CL * SEL_THREADS) {
@@ -1120,6 +1128,7 @@ __global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args 
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
   wait_previous_kernel();
+  allow_next_kernel();
   const int t0 = blockIdx.x * d.block, rows = min(d.block, lens2[b] - t0);
   if (rows <= 0) return;
   const size_t hd = (size_t)b * a.Hkv + g;
@@ -1186,12 +1195,10 @@ cudaError_t kv8_append(const Kv8Args& a, const void* kn, const void* vn, int is_
     return kv8::with_chunks(a.block, DH, [&](auto ch) {
       constexpr int CH = decltype(ch)::value;
       if (is_bf16)
-        kv8::append_kernel<bf16, DH, CH><<<grid, kv8::AP_THREADS, 0, s>>>(a, (const bf16*)kn, (const bf16*)vn, row_stride,
-                                                                         batch_stride, n, pos, count, status);
-      else
-        kv8::append_kernel<float, DH, CH><<<grid, kv8::AP_THREADS, 0, s>>>(a, (const float*)kn, (const float*)vn,
-                                                                          row_stride, batch_stride, n, pos, count, status);
-      return cudaGetLastError();
+        return launch_dependent(kv8::append_kernel<bf16, DH, CH>, grid, kv8::AP_THREADS, 0, s, a, (const bf16*)kn,
+                                (const bf16*)vn, row_stride, batch_stride, n, pos, count, status);
+      return launch_dependent(kv8::append_kernel<float, DH, CH>, grid, kv8::AP_THREADS, 0, s, a, (const float*)kn,
+                              (const float*)vn, row_stride, batch_stride, n, pos, count, status);
     });
   };
   return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
@@ -1204,9 +1211,8 @@ cudaError_t kv8_read(const Kv8Args& a, const int* first, const int* rows, int n,
     using T = decltype(type);
     constexpr int NC = decltype(nc)::value;
     const dim3 grid((chunks + 256 * NC - 1) / (256 * NC), 2 * a.Hkv, a.B);
-    kv8::read_kernel<T, decltype(dh)::value, NC><<<grid, 256, 0, s>>>(a, first, rows, n, (T*)k_out, (T*)v_out, row_stride,
-                                                                      batch_stride, status);
-    return cudaGetLastError();
+    return launch_dependent(kv8::read_kernel<T, decltype(dh)::value, NC>, grid, 256, 0, s, a, first, rows, n, (T*)k_out,
+                            (T*)v_out, row_stride, batch_stride, status);
   };
   // two chunks a thread once that still leaves every SM four blocks; fewer rows: more threads
   auto with_nc = [&](auto type, auto dh) {
@@ -1227,21 +1233,6 @@ static int kv8_grid(int R, int dh) {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = sms * (kv8_groups(R) == 2 && dh == 128 ? 2 : 3);
   return grid < kv8::MG_MOST ? grid : kv8::MG_MOST;
-}
-
-// A launch that may start while the kernel before it in the stream still runs (it waits for it itself).
-template <typename... P, typename... A>
-static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(threads);
-  c.stream = s;
-  c.attrs = &attr;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t* stats, size_t* scores) {
@@ -1270,14 +1261,13 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
     constexpr int smem = kv8::AtCfg<DH>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kv8::AT_THREADS, smem, s>>>(tk, tv, a, status);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_dependent(kernel, grid, kv8::AT_THREADS, smem, s, tk, tv, a, status)) != cudaSuccess) return e;
     // few ranges per unit: a warp per row
     const bool few = grid <= 8LL * a.c.B * a.c.Hkv * ((R + 8 * NT - 1) / (8 * NT));
     e = launch_dependent(few ? kv8::merge_kernel<T, DH, WT, 1> : kv8::merge_kernel<T, DH, WT, 8>,
-                         dim3(few ? (R + 7) / 8 : R, a.c.Hkv, a.c.B), kv8::MG_THREADS, s, a, 8 * NT, grid);
+                         dim3(few ? (R + 7) / 8 : R, a.c.Hkv, a.c.B), kv8::MG_THREADS, 0, s, a, 8 * NT, grid);
     if (e != cudaSuccess || !WT) return e;
-    return launch_dependent(kv8::weights_kernel, dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, s, a);
+    return launch_dependent(kv8::weights_kernel, dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, 0, s, a);
   };
   auto with_wt = [&](auto type, auto dh, auto nts) {
     return a.weights ? run(type, dh, nts, std::true_type()) : run(type, dh, nts, std::false_type());
@@ -1302,24 +1292,26 @@ cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, i
   while (cl < kv8::SEL_CLUSTER && cl * 4096 < a.Lmax && cl * a.B * a.Hkv <= sms) cl *= 2;
   cudaError_t e = cudaFuncSetAttribute(kv8::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kv8::SEL_SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cl;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(a.B * a.Hkv * cl);
   lc.blockDim = dim3(kv8::SEL_THREADS);
   lc.dynamicSmemBytes = kv8::SEL_SMEM;
   lc.stream = s;
-  lc.attrs = &attr;
-  lc.numAttrs = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
   e = cudaLaunchKernelEx(&lc, kv8::select_kernel, weights, a.Lmax, a.Hkv, cl, lens, keep, first, recent, kept, lens2);
   if (e != cudaSuccess) return e;
   const dim3 grid((keep + d.block - 1) / d.block, 2 * a.Hkv, a.B);
   auto run = [&](auto dh) {
     constexpr int DH = decltype(dh)::value;
     return kv8::with_chunks(d.block, DH, [&](auto ch) {
-      return launch_dependent(kv8::compact_kernel<DH, decltype(ch)::value>, grid, kv8::AP_THREADS, s, a, d, (const int*)kept, keep,
+      return launch_dependent(kv8::compact_kernel<DH, decltype(ch)::value>, grid, kv8::AP_THREADS, 0, s, a, d, (const int*)kept, keep,
                               (const int*)lens2, weights, weights2);
     });
   };

@@ -216,6 +216,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  if constexpr (WN) {
+    wait_previous_kernel();
+    allow_next_kernel();
+  }
   // TMEM column of O_t and of S_t / P_t
 #define O_COL(t) (128u * (uint32_t)(t))
 #define S_COL(t) (256u + 128u * (uint32_t)(t))
@@ -779,6 +783,7 @@ cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
   constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES : 0);
   cudaError_t e = set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
   if (e != cudaSuccess) return e;
+  if (MODE == 2) return launch_dependent(tca::attn_tc_kernel<DH, MODE>, grid, tca::NTHREADS, sm, s, tq, tk, tv, a, status);
   tca::attn_tc_kernel<DH, MODE><<<grid, tca::NTHREADS, sm, s>>>(tq, tk, tv, a, status);
   return cudaGetLastError();
 }

@@ -176,6 +176,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  // WN: launched beside attn_bwd_dkdv_kernel, which lets it start only once the kernels before that
+  // have ended; it shares nothing with it and waits for it at its own end
   constexpr uint32_t S_COL = 0, P_COL = 128, Q_COL = 256;  // S (then scale*dS), dP, dQ
 
   const int nqt = (a.S + BT - 1) / BT;
@@ -480,6 +482,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tmem_dealloc(tbase, TMEM_COLS);
     if (lane == 0) linger_after_abort(abort);  // copies issued before a role gave up land first
   }
+  if constexpr (WN) {
+    wait_previous_kernel();
+    allow_next_kernel();
+  }
 }
 
 // ============================================================================ dK, dV
@@ -540,6 +546,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  if constexpr (WN) {
+    wait_previous_kernel();
+    allow_next_kernel();
+  }
   constexpr uint32_t S_COL = 0, P_COL = 128, V_COL = 256, K_COL = 256 + DH;  // S^T/P^T, dP^T/dS^T, dV, dK
 
   const int nqt = (a.S + BT - 1) / BT;
@@ -915,6 +925,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // order.  One block per (sink, KV group, sequence), one thread per column of [dK | dV].
 __global__ void sink_sum_kernel(AttnBwdArgs a) {
   const int key = blockIdx.x, g = blockIdx.y, b = blockIdx.z, c = threadIdx.x;
+  wait_previous_kernel();
+  allow_next_kernel();
   const int len = used_rows(a, b);
   if (key >= len) return;
   const int used = (len + BT - 1) / BT, last = last_query_tile(a, key / BT, used);
@@ -932,6 +944,8 @@ __global__ void sink_sum_kernel(AttnBwdArgs a) {
 __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
                                                           const bf16* __restrict__ o, int ld_o, AttnBwdArgs a,
                                                           float* __restrict__ dsum) {
+  wait_previous_kernel();
+  allow_next_kernel();
   const int lane = threadIdx.x & 31, per = a.dh / 8, pieces = a.Hq * per;
   const long long tok = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (tok >= (long long)a.B * a.lse_ld) return;
@@ -966,9 +980,16 @@ static cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tdo, con
   cudaError_t e = set_max_smem(tcb::attn_bwd_dkdv_kernel<DH, WN>, C::SMEM_DKDV, s);
   if (e != cudaSuccess) return e;
   const int nkv = a.B * a.Hkv * (nqt + (WN ? a.sink_tiles * a.far_chunks : 0)), nq = a.B * a.Hq * nqt;
+  if ((e = set_max_smem(tcb::attn_bwd_dq_kernel<DH, WN>, C::SMEM_DQ, s)) != cudaSuccess) return e;
+  if (WN) {
+    e = launch_dependent(tcb::attn_bwd_dkdv_kernel<DH, WN>, nkv < sms ? nkv : sms, tcb::NTHREADS, C::SMEM_DKDV, s, tq, tdo,
+                         tk, tv, a, status);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(tcb::attn_bwd_dq_kernel<DH, WN>, nq < sms ? nq : sms, tcb::NTHREADS, C::SMEM_DQ, s, tq, tdo, tk,
+                            tv, a, status);
+  }
   tcb::attn_bwd_dkdv_kernel<DH, WN><<<nkv < sms ? nkv : sms, tcb::NTHREADS, C::SMEM_DKDV, s>>>(tq, tdo, tk, tv, a, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = set_max_smem(tcb::attn_bwd_dq_kernel<DH, WN>, C::SMEM_DQ, s)) != cudaSuccess) return e;
   tcb::attn_bwd_dq_kernel<DH, WN><<<nq < sms ? nq : sms, tcb::NTHREADS, C::SMEM_DQ, s>>>(tq, tdo, tk, tv, a, status);
   return cudaGetLastError();
 }
@@ -1027,9 +1048,8 @@ cudaError_t window_attention_backward_tc(const AttnBwdArgs& args, const AttnBwdS
   far_chunks(a);
   a.dsum = dsum;
   const long long warps = (long long)a.B * a.lse_ld;
-  tcb::window_dsum_kernel<<<(unsigned)((warps * 32 + 255) / 256), 256, 0, s>>>((const bf16*)a.dout, ld.dout, (const bf16*)o,
-                                                                               ld.o, a, dsum);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(tcb::window_dsum_kernel, (unsigned)((warps * 32 + 255) / 256), 256, 0, s,
+                                   (const bf16*)a.dout, ld.dout, (const bf16*)o, ld.o, a, dsum);
   CUtensorMap tq, tdo, tk, tv;
   const int rows = a.B * a.S;
   if (e == cudaSuccess) e = make_tmap_bf16(&tq, a.q, rows, a.Hq * a.dh, ld.q, tcb::BT);
@@ -1043,8 +1063,7 @@ cudaError_t window_attention_backward_tc(const AttnBwdArgs& args, const AttnBwdS
   e = a.dh == 128 ? launch_bwd<128, true>(tq, tdo, tk, tv, a, status, sms, s)
                   : launch_bwd<64, true>(tq, tdo, tk, tv, a, status, sms, s);
   if (e != cudaSuccess || !a.far_chunks) return e;
-  tcb::sink_sum_kernel<<<dim3(a.sinks, a.Hkv, a.B), 2 * a.dh, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(tcb::sink_sum_kernel, dim3(a.sinks, a.Hkv, a.B), 2 * a.dh, 0, s, a);
 }
 
 }  // namespace mka
