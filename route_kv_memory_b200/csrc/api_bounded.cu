@@ -295,7 +295,7 @@ int mka_window_attention_backward(const mka_attn_config* cfg, const mka_attn_str
   a.window = w.window; a.sinks = w.sinks; a.lens = lens;
   a.dq16 = dq; a.dk16 = dk; a.dv16 = dv;
   a.sink_part = (float*)((char*)ws + part);
-  CUDA_TRY(window_attention_backward_tc(a, w.ld, out, (float*)ws, status, (cudaStream_t)stream));
+  CUDA_TRY(window_attention_backward_tc(a, w.ld, out, ws, status, (cudaStream_t)stream));
   return MKA_OK;
 }
 

@@ -210,13 +210,15 @@ struct AttnBwdArgs {
   void *dq16 = nullptr, *dk16 = nullptr, *dv16 = nullptr;
   float* sink_part = nullptr;  // [B][Hkv][1 + far_chunks][sinks][2 dh] partial dK | dV of the sinks
   int sink_tiles = 0, far_chunks = 0, far_tiles = 1;  // set by window_attention_backward_tc
+  int* items = nullptr;  // in the scratch: items of dK/dV and of dQ handed out, items of dK/dV in `order`
+  int* order = nullptr;
 };
 cudaError_t attention_backward_tc(const AttnBwdArgs& a, int* status, cudaStream_t s);
 // Row strides (elements) of the windowed backward's operands; sequences are S rows apart.
 struct AttnBwdStrides { int q, k, v, o, dout; };
-// Scratch of the windowed backward: D, then (at *part) the sinks' partial sums.
+// Scratch of the windowed backward: item counters and D, then (at *part) the sinks' partial sums.
 size_t window_attention_backward_scratch(int B, int S, int Hq, int Hkv, int dh, int window, int sinks, size_t* part);
-cudaError_t window_attention_backward_tc(const AttnBwdArgs& a, const AttnBwdStrides& ld, const void* o, float* dsum,
+cudaError_t window_attention_backward_tc(const AttnBwdArgs& a, const AttnBwdStrides& ld, const void* o, void* ws,
                                          int* status, cudaStream_t s);
 // dsum[(b * Hq + h) * ld + t] = sum_i dO * O over head h of token t (bf16 inputs).
 cudaError_t attention_dsum(const void* dout, const void* o, int B, int S, int Hq, int dh, int ld, float* dsum,

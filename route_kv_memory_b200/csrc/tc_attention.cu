@@ -124,14 +124,32 @@ __device__ __forceinline__ int entry_token(int v, int S, int* slot) {
   return v >= 0 && t < S ? t : -1;
 }
 
+// MODE 2, padded batches: the items of rows in use only, sequence by sequence, longest pairs first, the
+// heads of a pair next to each other.  first[b]: the items in front of sequence b's (built per CTA from
+// lens; the static snake would otherwise give some CTAs mostly items behind the sequences' ends:
+// LENS_NOTE).
+constexpr int MAX_RAGGED = 512;  // sequences; more: every item is enumerated and the empty ones skipped
+__device__ __forceinline__ Work used_item(int w, const int* first, int B, int Hq) {
+  int lo = 0, hi = B;  // first[lo] <= w < first[hi]
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (first[m] <= w) lo = m;
+    else hi = m;
+  }
+  Work r;
+  r.b = lo;
+  r.pair = (first[lo + 1] - 1 - w) / Hq;
+  r.h = Hq - 1 - (first[lo + 1] - 1 - w) % Hq;
+  return r;
+}
 // MODE 2 work item: query tiles 2 pair and 2 pair + 1 of head h of sequence b (len rows in use).
 // Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
 struct WWork {
   int b, h, pair, len, lo, nsk, n0, n1, s1;
   __device__ __forceinline__ int key_tile(int j) const { return j == 0 ? lo : (j <= nsk ? j - 1 : lo + j - nsk); }
 };
-__device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, int npairs) {
-  const Work it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
+__device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, int npairs, const int* first) {
+  const Work it = first ? used_item(w, first, a.B, a.Hq) : work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
   WWork r;
   r.b = it.b;
   r.h = it.h;
@@ -227,7 +245,31 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int nqt = (a.S + BQ - 1) / BQ;
   const int npairs = (nqt + 1) / 2;
   const int nbj = a.B * a.nblk;
-  const int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : a.B * a.Hq * npairs;
+  int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : a.B * a.Hq * npairs;
+  const int* first = nullptr;  // MODE 2, padded batches: see used_item
+  if constexpr (WN) {
+    if (a.lens && a.B <= MAX_RAGGED) {
+      int* sfirst = (int*)(smem + 2 * C::Q_BYTES + 2 * C::KV_BYTES + 256);
+      if (warp == 0) {  // prefix sums of the sequences' items, 32 at a time
+        int sum = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+          const int b = b0 + lane, n = b < a.B ? (min(max(a.lens[b], 0), a.S) + 2 * BQ - 1) / (2 * BQ) * a.Hq : 0;
+          int inc = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+          }
+          if (b < a.B) sfirst[b] = sum + inc - n;
+          sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) sfirst[a.B] = sum;
+      }
+      __syncthreads();
+      first = sfirst;
+      nwork = sfirst[a.B];
+    }
+  }
   const int G = a.Hq / a.Hkv;
   const int RPT = gathered_rows_per_token(G);  // MODE 1: tile rows per token (its G heads first)
   const int tpt = BQ / RPT;                    // MODE 1: tokens per query tile
@@ -357,7 +399,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Work it;
         WWork ww;
         if constexpr (WN) {
-          ww = window_item(w, a, npairs);
+          ww = window_item(w, a, npairs, first);
           if (ww.n1 == 0) continue;  // (every role skips the same items)
           it = {ww.b, ww.h, ww.pair};
         } else {
@@ -449,7 +491,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       if constexpr (WN) {
-        ww = window_item(w, a, npairs);
+        ww = window_item(w, a, npairs, first);
         if (ww.n1 == 0) continue;
         nx0 = ww.n0;
         nx1 = ww.n1;
@@ -553,7 +595,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       WWork ww;
       int j0 = 0;  // first step of this tile
       if constexpr (WN) {
-        ww = window_item(w, a, npairs);
+        ww = window_item(w, a, npairs, first);
         if (ww.n1 == 0) continue;
       }
       const int wi = done++;
@@ -780,7 +822,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 template <int DH, int MODE>
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                         int* status, int grid, cudaStream_t s) {
-  constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES : 0);
+  constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES
+                                          : MODE == 2 ? (tca::MAX_RAGGED + 4) * 4 : 0);
   cudaError_t e = set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
   if (e != cudaSuccess) return e;
   if (MODE == 2) return launch_dependent(tca::attn_tc_kernel<DH, MODE>, grid, tca::NTHREADS, sm, s, tq, tk, tv, a, status);

@@ -110,10 +110,75 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttnBwdArgs& a, int qt) {
   k.n = k.nsk + qt - k.lo + 1;
   return k;
 }
+// WN: work items are handed out by a counter in the scratch (D's kernel zeroes it): dQ's CTAs start as
+// dK/dV's leave, so no static split fits, and neither does one over sequences of different lengths.  The
+// loader takes an item once it has loaded all of the one before (two steps ahead of the compute warps, so
+// the counter's latency is hidden and no CTA sits on a second item), and passes it on through two slots.
+struct ItemSlots {
+  uint64_t *full, *empty;  // [2], counts 1 and 1 + NCOMPUTE (the MMA warp and the compute warps)
+  volatile int* item;      // [2]
+};
+__device__ __forceinline__ void init_slots(const ItemSlots& s) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&s.full[i], 1);
+    mbar_init(&s.empty[i], 1 + NCOMPUTE);
+  }
+}
+// Loader thread: passes on the next item that is not `dead` as the rr-th (-1: no more).  Returns it, or -2
+// when the kernel unwinds.  order (nullable): the items in the order to give them.
+template <typename F>
+__device__ __forceinline__ int give_item(const ItemSlots& s, int rr, int* counter, int nwork, F dead,
+                                         const int* order, volatile int* abort, int* status) {
+  int w;
+  do {
+    w = atomicAdd(counter, 1);
+    w = w < nwork ? w : -1;
+  } while (w >= 0 && dead(w));
+  if (order && w >= 0) w = order[w];
+  if (!mbar_wait(&s.empty[rr & 1], ((rr >> 1) & 1) ^ 1, abort, status)) return -2;
+  s.item[rr & 1] = w;
+  mbar_arrive(&s.full[rr & 1]);
+  return w;
+}
+// The other warps (whole warp): the rr-th item.
+__device__ __forceinline__ int take_item(const ItemSlots& s, int rr, int lane, volatile int* abort, int* status) {
+  if (!mbar_wait_warp(&s.full[rr & 1], (rr >> 1) & 1, abort, status)) return -2;
+  const int w = s.item[rr & 1];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&s.empty[rr & 1]);
+  return w;
+}
+
 // WN: last query tile whose window reaches key tile kt, and the far chunks of a sink tile behind it.
 __device__ __forceinline__ int last_query_tile(const AttnBwdArgs& a, int kt, int nqt_used) {
   if (!a.window) return nqt_used - 1;
   return min(nqt_used - 1, (kt * BT + BT - 1 + a.window - 1) / BT);
+}
+
+// WN: item w of dK/dV: the key tile kt of (sequence b, KV group g) with the query tiles [q0, q0 + nq) that
+// see it (nq == 0: none).  The far items of the sink tiles come first; slot: place among a sink tile's
+// partial sums, 0 for the tile's own item, 1 + chunk for a far one.
+struct KvItem {
+  int b, g, kt, q0, nq, slot, len;
+};
+__device__ __forceinline__ int kv_items(const AttnBwdArgs& a) {
+  return a.B * a.Hkv * (a.sink_tiles * a.far_chunks + (a.S + BT - 1) / BT);
+}
+__device__ __forceinline__ KvItem kv_item(const AttnBwdArgs& a, int w) {
+  KvItem x;
+  const int per = a.B * a.Hkv, nfar = a.sink_tiles * a.far_chunks, t = w / per, bg = w % per;
+  const bool far = t < nfar;
+  const int chunk = far ? t / a.sink_tiles : 0;
+  x.kt = far ? t % a.sink_tiles : t - nfar;
+  x.b = bg / a.Hkv;
+  x.g = bg % a.Hkv;
+  x.slot = far ? 1 + chunk : 0;
+  x.len = used_rows(a, x.b);
+  const int used = (x.len + BT - 1) / BT;  // query tiles with rows in use
+  const int last = last_query_tile(a, x.kt, used);
+  x.q0 = far ? last + 1 + chunk * a.far_tiles : x.kt;
+  x.nq = x.kt >= used ? 0 : max(0, far ? min(a.far_tiles, used - x.q0) : last - x.kt + 1);
+  return x;
 }
 
 // ============================================================================ dQ
@@ -148,6 +213,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* s_free = s_full + 5;   // the compute warps hold S in registers: its columns are free
   uint64_t* dp_full = s_full + 6;  // dP has landed
   uint32_t* tmem_slot = (uint32_t*)(s_full + 7);
+  const ItemSlots slots = {s_full + 8, s_full + 10, (volatile int*)(s_full + 12)};
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -168,6 +234,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(s_free, NCOMPUTE);
     mbar_init(dp_full, 1);
     mbar_init(drain, 1);
+    if (WN) init_slots(slots);
     *abort = 0;
     fence_barrier_init();
   }
@@ -198,20 +265,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_prefetch_desc(&tmdO);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
-      int kvit = 0, done = 0;
+      int kvit = 0;
       bool ok = true;
       for (int rr = 0; ok; ++rr) {
-        const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
+        int w, b, h, qt;
+        if constexpr (WN) {
+          w = give_item(slots, rr, a.items + 1, nwork, [&](int x) {
+            item(x, b, h, qt);
+            return qt * BT >= used_rows(a, b);
+          }, nullptr, abort, status);
+        } else {
+          w = snake(rr, gridDim.x, blockIdx.x, nwork);
+        }
         if (w < 0) break;
-        int b, h, qt;
         item(w, b, h, qt);
         KeyTiles kl;
-        if constexpr (WN) {
-          if (qt * BT >= used_rows(a, b)) continue;  // (every role skips the same items)
-          kl = key_tiles(a, qt);
-        }
-        const int n = WN ? kl.n : qt + 1, it = done++;
-        if (!mbar_wait(q_empty, (it & 1) ^ 1, abort, status)) break;
+        if constexpr (WN) kl = key_tiles(a, qt);
+        const int n = WN ? kl.n : qt + 1;
+        if (!mbar_wait(q_empty, (rr & 1) ^ 1, abort, status)) break;
         mbar_expect_tx(q_full, 2 * C::TILE);
         for (int hb = 0; hb < C::NH; ++hb) {
           tma_load_2d(sQ + hb * C::HALF, &tmQ, q_full, h * DH + hb * 64, b * a.S + qt * BT);
@@ -239,7 +310,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp == 1) {  // the whole warp runs the MMA role; one elected lane issues
     const uint64_t qd = sdesc_kmajor_sw128(sQ), dod = sdesc_kmajor_sw128(sdO);
-    int kvit = 0, pc = 0, sf = 0, done = 0, len = 0;
+    int kvit = 0, pc = 0, sf = 0, len = 0;
     bool ok = true, first = true;
     KeyTiles kl = {};
     // K (V) of step j has landed in its ring slot; WN clears its rows at or past the sequence's end:
@@ -284,17 +355,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // S(j+1) goes in as soon as the compute warps hold S(j) in registers, so their exponentials
     // of tile j+1 run under dQ(j) and dP(j+1); dP(j+1) follows dQ(j), which reads dS(j) over dP.
     for (int rr = 0; ok; ++rr) {
-      const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
+      const int w = WN ? take_item(slots, rr, lane, abort, status) : snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       int b, h, qt;
       item(w, b, h, qt);
       if constexpr (WN) {
         len = used_rows(a, b);
-        if (qt * BT >= len) continue;
         kl = key_tiles(a, qt);
       }
-      const int n = WN ? kl.n : qt + 1, it = done++;
-      if (!mbar_wait_warp(q_full, it & 1, abort, status)) break;
+      const int n = WN ? kl.n : qt + 1;
+      if (!mbar_wait_warp(q_full, rr & 1, abort, status)) break;
       if (!k_ready(kvit, 0)) break;
       if (!first) {
         if (!mbar_wait_warp(s_free, sf & 1, abort, status)) break;
@@ -318,7 +388,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!mbar_wait_warp(p_full, pc & 1, abort, status)) { ok = false; break; }
         ++pc;
-        if (j == 0 && !mbar_wait_warp(dq_empty, (it & 1) ^ 1, abort, status)) { ok = false; break; }
+        if (j == 0 && !mbar_wait_warp(dq_empty, (rr & 1) ^ 1, abort, status)) { ok = false; break; }
         tc_fence_after();
         issue_dq(cur % C::KST, j > 0);
         umma_commit_w(&k_empty[cur % C::KST]);
@@ -346,19 +416,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t s_tmem = tbase + lane_off + S_COL, p_tmem = tbase + lane_off + P_COL;
     const uint32_t q_tmem = tbase + lane_off + Q_COL + half * (DH / 2);
     const float sl2 = a.scale * 1.4426950408889634f, l2scale = log2f(a.scale);
-    int sit = 0, done = 0;
+    int sit = 0;
     for (int rr = 0;; ++rr) {
-      const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
+      const int w = WN ? take_item(slots, rr, lane, abort, status) : snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       int b, h, qt, len = a.S;
       item(w, b, h, qt);
       KeyTiles kl;
       if constexpr (WN) {
         len = used_rows(a, b);
-        if (qt * BT >= len) continue;
         kl = key_tiles(a, qt);
       }
-      const int n = WN ? kl.n : qt + 1, row = qt * BT + r, it = done++;
+      const int n = WN ? kl.n : qt + 1, row = qt * BT + r;
       const bool valid = row < len;
       const size_t li = ((size_t)b * a.Hq + h) * a.lse_ld + (valid ? row : 0);
       // scale * P = 2^(s sl2 - lse + log2 scale): dQ's factor scale rides in the exponent
@@ -430,7 +499,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
-      if (!mbar_wait_warp(dq_full, it & 1, abort, status)) break;
+      if (!mbar_wait_warp(dq_full, rr & 1, abort, status)) break;
       tc_fence_after();
       if constexpr (WN) {
         bf16* dst = (bf16*)a.dq16 + ((size_t)b * a.S + (valid ? row : 0)) * (size_t)(a.Hq * DH) + (size_t)h * DH +
@@ -520,6 +589,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* s_free = bars + 15;   // the compute warps hold S^T in registers: its columns are free
   uint64_t* dp_full = bars + 16;  // dP^T has landed
   uint32_t* tmem_slot = (uint32_t*)(bars + 17);
+  const ItemSlots slots = {bars + 18, bars + 20, (volatile int*)(bars + 22)};
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -538,6 +608,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(s_free, NCOMPUTE);
     mbar_init(dp_full, 1);
     mbar_init(drain, 1);
+    if (WN) init_slots(slots);
     *abort = 0;
     fence_barrier_init();
   }
@@ -553,8 +624,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr uint32_t S_COL = 0, P_COL = 128, V_COL = 256, K_COL = 256 + DH;  // S^T/P^T, dP^T/dS^T, dV, dK
 
   const int nqt = (a.S + BT - 1) / BT;
-  const int nfar = WN ? a.B * a.Hkv * a.sink_tiles * a.far_chunks : 0;  // WN: far items of the sink tiles come first
-  const int nwork = nfar + a.B * a.Hkv * nqt;
+  const int nwork = WN ? a.items[2] : a.B * a.Hkv * nqt;
   const int G = a.Hq / a.Hkv;
   // item w: key tile kt (longest first: the most query tiles), KV group g, sequence b; its steps
   // run the G heads (outer) over the query tiles kt..nqt-1 (inner)
@@ -565,32 +635,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     g = rem % a.Hkv;
     b = rem / a.Hkv;
   };
-  // The item with its query tiles [q0, q0 + nq) (nq == 0: nothing to do, every role skips it) and, WN,
-  // its slot among a sink tile's partial sums: 0 for the tile's own item, 1 + chunk for a far one.
+  // The item with its query tiles [q0, q0 + nq) and, WN, its slot among a sink tile's partial sums
   auto steps = [&](int w, int& b, int& g, int& kt, int& q0, int& nq, int& slot, int& len) {
-    slot = 0;
     if constexpr (WN) {
-      const bool far = w < nfar;
-      int chunk = 0;
-      if (far) {
-        const int per = a.B * a.Hkv;
-        chunk = w / per / a.sink_tiles;
-        kt = w / per % a.sink_tiles;
-        g = w % per % a.Hkv;
-        b = w % per / a.Hkv;
-        slot = 1 + chunk;
-      } else {
-        item(w - nfar, b, g, kt);
-      }
-      len = used_rows(a, b);
-      const int used = (len + BT - 1) / BT;  // query tiles with rows in use
-      const int last = last_query_tile(a, kt, used);
-      q0 = far ? last + 1 + chunk * a.far_tiles : kt;
-      nq = kt >= used ? 0 : max(0, far ? min(a.far_tiles, used - q0) : last - kt + 1);
+      const KvItem x = kv_item(a, w);
+      b = x.b; g = x.g; kt = x.kt; q0 = x.q0; nq = x.nq; slot = x.slot; len = x.len;
     } else {
       item(w, b, g, kt);
       q0 = kt;
       nq = nqt - kt;
+      slot = 0;
       len = a.S;
     }
   };
@@ -601,16 +655,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_prefetch_desc(&tmdO);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
-      int qdit = 0, done = 0;
+      int qdit = 0;
       bool ok = true;
       for (int rr = 0; ok; ++rr) {
-        const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
+        int w, b, g, kt, qs, nq, slot, len;
+        if constexpr (WN) {
+          w = give_item(slots, rr, a.items, nwork, [](int) { return false; }, a.order, abort, status);
+        } else {
+          w = snake(rr, gridDim.x, blockIdx.x, nwork);
+        }
         if (w < 0) break;
-        int b, g, kt, qs, nq, slot, len;
         steps(w, b, g, kt, qs, nq, slot, len);
-        if (WN && nq == 0) continue;
-        const int it = done++;
-        if (!mbar_wait(kv_empty, (it & 1) ^ 1, abort, status)) break;
+        if (!mbar_wait(kv_empty, (rr & 1) ^ 1, abort, status)) break;
         mbar_expect_tx(kv_full, 2 * C::TILE);
         for (int hb = 0; hb < C::NH; ++hb) {
           tma_load_2d(sK + hb * C::HALF, &tmK, kv_full, g * DH + hb * 64, b * a.S + kt * BT);
@@ -641,7 +697,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else if (warp == 1) {  // the whole warp runs the MMA role; one elected lane issues
     const uint64_t kd = sdesc_kmajor_sw128(sK), vd = sdesc_kmajor_sw128(sV);
-    int qdit = 0, pc = 0, sf = 0, done = 0;
+    int qdit = 0, pc = 0, sf = 0;
     bool ok = true, first = true;
     int used = BT;  // WN: rows in use of the item's last query tile, cleared behind (dK, dV sum over queries)
     auto q_ready = [&](int cur, bool end) {
@@ -696,14 +752,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // exponentials of step s+1 run under dV / dK(s) and dP^T(s+1); dP^T(s+1) follows dV / dK(s),
     // which read P^T(s) and dS^T(s) over the dP^T columns.
     for (int rr = 0; ok; ++rr) {
-      const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
+      const int w = WN ? take_item(slots, rr, lane, abort, status) : snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       int b, g, kt, qs, nq, slot, len;
       steps(w, b, g, kt, qs, nq, slot, len);
-      if (WN && nq == 0) continue;
-      const int n = G * nq, it = done++;
+      const int n = G * nq;
       if constexpr (WN) used = min(BT, len - (qs + nq - 1) * BT);
-      if (!mbar_wait_warp(kv_full, it & 1, abort, status)) break;
+      if (!mbar_wait_warp(kv_full, rr & 1, abort, status)) break;
       if (!q_ready(qdit, nq == 1)) break;
       if (!first) {
         if (!mbar_wait_warp(s_free, sf & 1, abort, status)) break;
@@ -727,7 +782,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!mbar_wait_warp(p_full, pc & 1, abort, status)) { ok = false; break; }
         ++pc;
-        if (s == 0 && !mbar_wait_warp(acc_empty, (it & 1) ^ 1, abort, status)) { ok = false; break; }
+        if (s == 0 && !mbar_wait_warp(acc_empty, (rr & 1) ^ 1, abort, status)) { ok = false; break; }
         tc_fence_after();
         issue_acc(st, s > 0);
         if (s + 1 < n) {
@@ -753,14 +808,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_tmem = tbase + lane_off + S_COL, p_tmem = tbase + lane_off + P_COL;
     const float sl2 = a.scale * 1.4426950408889634f;
-    int sit = 0, done = 0;
+    int sit = 0;
     for (int rr = 0;; ++rr) {
-      const int w = snake(rr, gridDim.x, blockIdx.x, nwork);
+      const int w = WN ? take_item(slots, rr, lane, abort, status) : snake(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       int b, g, kt, qs, nq, slot, len;
       steps(w, b, g, kt, qs, nq, slot, len);
-      if (WN && nq == 0) continue;
-      const int n = G * nq, key = kt * BT + r, it = done++;
+      const int n = G * nq, key = kt * BT + r;
       // WN: queries at or past this position do not see the key
       const int until = WN && a.window && key >= a.sinks ? min(len, key + a.window) : len;
       bool ok = true;
@@ -843,7 +897,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive(p_full);
       }
       if (!ok) break;
-      if (!mbar_wait_warp(acc_full, it & 1, abort, status)) break;
+      if (!mbar_wait_warp(acc_full, rr & 1, abort, status)) break;
       tc_fence_after();
       const bool valid = key < len;
       if constexpr (WN) {
@@ -939,6 +993,7 @@ __global__ void sink_sum_kernel(AttnBwdArgs a) {
   else ((bf16*)a.dv16)[at + c - a.dh] = __float2bfloat16_rn(acc);
 }
 
+constexpr int PLAN_BINS = 1024;  // lengths of dK/dV items told apart
 // WN: dsum[(b * Hq + h) * ld + t] = sum_i dO * O over head h of token t, 0 for t >= lens[b] up to ld.
 // A warp per (token, 32 pieces of 16 bytes): 2 (d_head 128) or 4 heads; any row strides.
 __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
@@ -947,7 +1002,40 @@ __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict
   wait_previous_kernel();
   allow_next_kernel();
   const int lane = threadIdx.x & 31, per = a.dh / 8, pieces = a.Hq * per;
-  const long long tok = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const long long tok = ((long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x) >> 5;
+  if (blockIdx.x == 0) {  // the plan: counters, and the items of dK/dV that have steps, longest first
+    __shared__ int at[PLAN_BINS];
+    const int n = kv_items(a);
+    for (int i = threadIdx.x; i < PLAN_BINS; i += 256) at[i] = 0;
+    if (threadIdx.x < 2) a.items[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const int nq = kv_item(a, i).nq;
+      if (nq) atomicAdd(&at[PLAN_BINS - min(nq, PLAN_BINS)], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {  // counts to first places, 32 bins at a time
+      int sum = 0;
+      for (int i = lane; i < PLAN_BINS; i += 32) {
+        const int v = at[i];
+        int inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        at[i] = sum + inc - v;
+        sum += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      if (lane == 0) a.items[2] = sum;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const int nq = kv_item(a, i).nq;
+      if (nq) a.order[atomicAdd(&at[PLAN_BINS - min(nq, PLAN_BINS)], 1)] = i;
+    }
+    return;
+  }
   if (tok >= (long long)a.B * a.lse_ld) return;
   const int b = (int)(tok / a.lse_ld), t = (int)(tok % a.lse_ld);
   const bool in = t < used_rows(a, b);
@@ -1029,26 +1117,34 @@ static void far_chunks(AttnBwdArgs& a) {
   a.far_chunks = (nqt - 1 - reach + a.far_tiles - 1) / a.far_tiles;
 }
 
+constexpr size_t kItemBytes = 256;  // the item counters; then the items' order, then D
+static size_t plan_bytes(int B, int Hkv, int S, const AttnBwdArgs& a) {
+  return ((size_t)B * Hkv * (a.sink_tiles * a.far_chunks + (S + tcb::BT - 1) / tcb::BT) * 4 + 255) / 256 * 256;
+}
+
 size_t window_attention_backward_scratch(int B, int S, int Hq, int Hkv, int dh, int window, int sinks, size_t* part) {
   AttnBwdArgs a = {};
   a.S = S; a.window = window; a.sinks = sinks;
   far_chunks(a);
-  const size_t d = ((size_t)B * Hq * ((S + 127) / 128 * 128) * 4 + 255) / 256 * 256;
+  const size_t d = kItemBytes + plan_bytes(B, Hkv, S, a) + ((size_t)B * Hq * ((S + 127) / 128 * 128) * 4 + 255) / 256 * 256;
   if (part) *part = d;
   return d + (a.far_chunks ? (size_t)B * Hkv * (1 + a.far_chunks) * sinks * 2 * dh * 4 : 0);
 }
 
-cudaError_t window_attention_backward_tc(const AttnBwdArgs& args, const AttnBwdStrides& ld, const void* o, float* dsum,
+cudaError_t window_attention_backward_tc(const AttnBwdArgs& args, const AttnBwdStrides& ld, const void* o, void* ws,
                                          int* status, cudaStream_t s) {
   AttnBwdArgs a = args;
+  a.items = (int*)ws;
+  a.order = (int*)((char*)ws + kItemBytes);
+  far_chunks(a);
+  float* dsum = (float*)((char*)ws + kItemBytes + plan_bytes(a.B, a.Hkv, a.S, a));
   if (a.B <= 0 || a.S <= 0) return cudaSuccess;
   if ((a.dh != 64 && a.dh != 128) || a.Hq % a.Hkv || a.lse_ld < (a.S + tcb::BT - 1) / tcb::BT * tcb::BT || a.window < 0 ||
       a.sinks < 0 || a.sinks > a.S || a.window > a.S || (long long)a.B * a.S >= (1LL << 31))
     return cudaErrorInvalidValue;
-  far_chunks(a);
   a.dsum = dsum;
   const long long warps = (long long)a.B * a.lse_ld;
-  cudaError_t e = launch_dependent(tcb::window_dsum_kernel, (unsigned)((warps * 32 + 255) / 256), 256, 0, s,
+  cudaError_t e = launch_dependent(tcb::window_dsum_kernel, (unsigned)(1 + (warps * 32 + 255) / 256), 256, 0, s,
                                    (const bf16*)a.dout, ld.dout, (const bf16*)o, ld.o, a, dsum);
   CUtensorMap tq, tdo, tk, tv;
   const int rows = a.B * a.S;
