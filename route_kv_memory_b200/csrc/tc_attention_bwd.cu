@@ -993,7 +993,7 @@ __global__ void sink_sum_kernel(AttnBwdArgs a) {
   else ((bf16*)a.dv16)[at + c - a.dh] = __float2bfloat16_rn(acc);
 }
 
-constexpr int PLAN_BINS = 1024;  // lengths of dK/dV items told apart
+constexpr int PLAN_BINS = 128;  // lengths of dK/dV items told apart
 // WN: dsum[(b * Hq + h) * ld + t] = sum_i dO * O over head h of token t, 0 for t >= lens[b] up to ld.
 // A warp per (token, 32 pieces of 16 bytes): 2 (d_head 128) or 4 heads; any row strides.
 __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
@@ -1006,12 +1006,14 @@ __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict
   if (blockIdx.x == 0) {  // the plan: counters, and the items of dK/dV that have steps, longest first
     __shared__ int at[PLAN_BINS];
     const int n = kv_items(a);
+    int sh = 0;  // lengths are told apart in steps of 2^sh query tiles
+    while (((a.S + BT - 1) / BT >> sh) >= PLAN_BINS) ++sh;
     for (int i = threadIdx.x; i < PLAN_BINS; i += 256) at[i] = 0;
     if (threadIdx.x < 2) a.items[threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += 256) {
       const int nq = kv_item(a, i).nq;
-      if (nq) atomicAdd(&at[PLAN_BINS - min(nq, PLAN_BINS)], 1);
+      if (nq) atomicAdd(&at[PLAN_BINS - 1 - (nq >> sh)], 1);
     }
     __syncthreads();
     if (threadIdx.x < 32) {  // counts to first places, 32 bins at a time
@@ -1032,7 +1034,7 @@ __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += 256) {
       const int nq = kv_item(a, i).nq;
-      if (nq) a.order[atomicAdd(&at[PLAN_BINS - min(nq, PLAN_BINS)], 1)] = i;
+      if (nq) a.order[atomicAdd(&at[PLAN_BINS - 1 - (nq >> sh)], 1)] = i;
     }
     return;
   }
