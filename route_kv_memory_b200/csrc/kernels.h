@@ -302,8 +302,8 @@ struct Kv8Attn {
   float sl2;                 // score scale * log2(e)
   float* part;               // partial results
   float* weights;            // [B][Hkv][Lmax], nullable: += each token's summed softmax weight
-  float* stats;              // [B][Hkv][G n][2] with weights: each row's maximum (log2) and sum
-  float* scores;             // [B][Hkv][Lmax][G n] with weights: raw scores (log2 units)
+  float* stats;              // [B][Hkv][G n][2] with weights: maximum (log2) and sum of the rows of unsplit units
+  float* scores;             // [B][Hkv][Lmax][rows, padded to whole groups] with weights: raw scores (log2 units)
 };
 size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t* stats, size_t* scores);
 cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream_t s);

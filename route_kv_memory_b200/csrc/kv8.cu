@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(Kv8Args a, const T* 
   __shared__ float red[AP_THREADS / 32];
   constexpr int CPR = DH / 16;  // chunks per row
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
-  wait_previous_kernel();
   allow_next_kernel();
+  wait_previous_kernel();
   const int p = pos[b], c = count ? min(max(count[b], 0), n) : n;
   if (p < 0 || (long long)p + c > a.Lmax) {  // the whole sequence is left as it was
     if (threadIdx.x == 0) set_status(status, p < 0 ? kStatusBounds : kStatusCapacity);
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
                                                    T* v_out, long long row_stride, long long batch_stride, int* status) {
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
-  wait_previous_kernel();
   allow_next_kernel();
+  wait_previous_kernel();
   const int f = first ? first[b] : 0, r = rows ? min(max(rows[b], 0), n) : n;
   if (f < 0 || (long long)f + r > a.Lmax) {
     if (threadIdx.x == 0) set_status(status, kStatusBounds);
@@ -544,10 +544,14 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = j0 + 16 * h + 8 * (i >> 1) + slot_token<DH>(g8), r = rg * RT + t * 8 + 2 * c4 + (i & 1);
-              const float x = s[h][t][i] == -INFINITY ? -INFINITY : s[h][t][i] * (kf[h] * rf[t][i & 1]);
-              if (j < ts.len && r < R) a.scores[(hd * a.c.Lmax + j) * R + r] = x;
+            for (int i = 0; i < 2; ++i) {  // the two rows of a token; a token's rows are padded to whole groups
+              const int j = j0 + 16 * h + 8 * i + slot_token<DH>(g8);
+              float2 x = make_float2(s[h][t][2 * i] * (kf[h] * rf[t][0]), s[h][t][2 * i + 1] * (kf[h] * rf[t][1]));
+              if (edge) {  // (a hidden score times a factor of 0 would be NaN)
+                if (s[h][t][2 * i] == -INFINITY) x.x = -INFINITY;
+                if (s[h][t][2 * i + 1] == -INFINITY) x.y = -INFINITY;
+              }
+              if (j < ts.len) *(float2*)(a.scores + (hd * a.c.Lmax + j) * (nrg * RT) + rg * RT + t * 8 + 2 * c4) = x;
             }
       }
       // scores in log2 units are s * f; two references per row, for the sum (ml) and, with the exponent
@@ -752,8 +756,86 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
   if (threadIdx.x == 0) linger_after_abort(abort);  // a wait ran out: this CTA's copies land first
 }
 
+// The ranges' records of one unit's query rows.
+struct Records {
+  const float* p;  // the first range's record of row 0 of the row group: maximum, sum, reference of O, -, O
+  size_t step;     // to the next range's
+  int n;           // ranges; 1: the unit's CTA wrote its rows (and stats) itself
+};
+__device__ __forceinline__ Records unit_records(const Kv8Attn& a, int RT, int DH, int grid, long long before,
+                                                long long total, int b, int u, int upb, int tiles) {
+  const long long share = (total + grid - 1) / grid, start = before + (long long)u * tiles, end = start + tiles - 1;
+  const int c0 = (int)(start / share);
+  return {a.part + ((size_t)b * upb + u + c0) * RT * (DH + 4), (size_t)RT * (DH + 4), (int)(end / share) - c0 + 1};
+}
+
+// weights[b][g][j] += sum over the query rows of KV head g of their softmax weight of token j, from the raw
+// scores (log2 units) and each row's maximum and sum, which every CTA joins from the records for itself.
+// A block takes WG_TILES of the unit's tiles, a thread WG_TOKENS tokens 256 apart.
+constexpr int WG_THREADS = 256;  // = MG_THREADS
+constexpr int WG_TOKENS = 4, WG_TILES = WG_TOKENS * WG_THREADS / TILE;
+__device__ __forceinline__ void add_weights(const Kv8Attn& a, int RT, int DH, int grid, long long before, long long total,
+                                            int block, int g, int b, const Tiles& ts) {
+  using sm100::ex2;
+  constexpr int ROWS = 64;  // rows whose normalisers are in shared memory at a time
+  __shared__ __align__(16) float lse[ROWS];  // maximum + log2(sum)
+  const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t hd = (size_t)b * a.c.Hkv + g;
+  int j[WG_TOKENS];  // positions; -1: none
+  float w[WG_TOKENS] = {};
+#pragma unroll
+  for (int k = 0; k < WG_TOKENS; ++k) {
+    const int i = WG_TILES * block + 2 * k + (threadIdx.x >> 7), p = i < ts.n ? ts.tile(i) * TILE + (threadIdx.x & 127) : -1;
+    j[k] = p < ts.len ? p : -1;
+  }
+  for (int r0 = 0; r0 < R; r0 += ROWS) {
+    const int m = min(ROWS, (R - r0 + 3) & ~3);  // (rows behind R: the padding of the scores, weighed 0)
+    __syncthreads();
+    for (int r = warp; r < m; r += WG_THREADS / 32) {
+      const int row = r0 + r, rg = row / RT;
+      float L = -INFINITY, sum = 0.f;
+      if (row < R) {
+        const Records rec = unit_records(a, RT, DH, grid, before, total, b, g * nrg + rg, upb, ts.n);
+        if (rec.n == 1) {
+          if (lane == 0) {
+            const float2 x = *(const float2*)(a.stats + 2 * (hd * R + row));
+            L = x.x;
+            sum = x.y;
+          }
+        } else {
+          for (int c = lane; c < rec.n; c += 32) {
+            const float2 h = *(const float2*)(rec.p + c * rec.step + (size_t)(row % RT) * (DH + 4));
+            const float nl = fmaxf(L, h.x);
+            sum = (L == -INFINITY ? sum : sum * ex2(L - nl)) + (h.x == -INFINITY ? h.y : h.y * ex2(h.x - nl));
+            L = nl;
+          }
+        }
+        const float all = warp_max(L);
+        sum = warp_sum(L == -INFINITY ? sum : sum * ex2(L - all));
+        L = all;
+      }
+      // (a row that sees nothing: every score -inf, weighed 0 by any finite normaliser)
+      if (lane == 0) lse[r] = row >= R ? INFINITY : L == -INFINITY && sum == 0.f ? 0.f : L + log2f(sum);
+    }
+    __syncthreads();
+    for (int r = 0; r < m; r += 4) {
+      const float4 x = *(const float4*)(lse + r);
+#pragma unroll
+      for (int k = 0; k < WG_TOKENS; ++k)
+        if (j[k] >= 0) {
+          const float4 y = *(const float4*)(a.scores + (hd * a.c.Lmax + j[k]) * (size_t)(nrg * RT) + r0 + r);
+          w[k] += ex2(y.x - x.x) + ex2(y.y - x.y) + ex2(y.z - x.z) + ex2(y.w - x.w);
+        }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < WG_TOKENS; ++k)
+    if (j[k] >= 0) a.weights[hd * a.c.Lmax + j[k]] += w[k];
+}
+
 // Joins the partial results of the query rows; a unit without tiles gives 0.  WPR warps per row: 8 (a CTA
-// per row) where a unit lies over many CTAs' ranges, 1 (8 rows a CTA) where it lies over a few.
+// per row) where a unit lies over many CTAs' ranges, 1 (8 rows a CTA) where it lies over a few.  WT: the
+// blocks behind the rows' add up the weights.
 constexpr int MG_THREADS = 256;
 constexpr int MG_MOST = 1024;  // CTAs of the attention at most
 template <typename T, int DH, bool WT, int WPR>
@@ -767,7 +849,6 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
   const int R = a.G * a.n, nrg = (R + RT - 1) / RT, upb = a.c.Hkv * nrg;
   const int row = blockIdx.x * (NW / WPR) + warp / WPR, g = blockIdx.y, b = blockIdx.z, rg = row / RT, r = row % RT;
   const int u = g * nrg + rg;
-  const size_t hd = (size_t)b * a.c.Hkv + g;
   allow_next_kernel();
   const Tiles ts = unit_tiles(a, b);  // (lens is older than the attention, which waited before it started)
   long long before = 0, total = 0;
@@ -791,6 +872,13 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
   }
   // every CTA waits, so that this kernel's end means the attention's too
   wait_previous_kernel();
+  if constexpr (WT) {
+    const int rows = (R + NW / WPR - 1) / (NW / WPR);  // blocks of rows
+    if (blockIdx.x >= rows) {
+      if (WG_TILES * (blockIdx.x - rows) < ts.n) add_weights(a, RT, DH, grid, before, total, blockIdx.x - rows, g, b, ts);
+      return;
+    }
+  }
   if (row >= R) return;  // (WPR 8: never; WPR 1: no barrier follows)
   T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) + (size_t)(g * a.G + row % a.G) * DH +
            lane * PER;
@@ -799,11 +887,11 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
     for (int k = 0; k < PER; ++k) out[k] = from_f<T>(0.f);
     return;
   }
-  const long long share = (total + grid - 1) / grid, start = before + (long long)u * ts.n, end = start + ts.n - 1;
-  const int c0 = (int)(start / share), nrec = (int)(end / share) - c0 + 1;
+  const Records rec = unit_records(a, RT, DH, grid, before, total, b, u, upb, ts.n);
+  const int nrec = rec.n;
   if (nrec == 1) return;  // written whole by its CTA
-  const size_t step = (size_t)RT * (DH + 4);
-  const float* rec0 = a.part + (((size_t)b * upb + u + c0) * RT + r) * (DH + 4);
+  const size_t step = rec.step;
+  const float* rec0 = rec.p + (size_t)r * (DH + 4);
   // this warp's records sub, sub + WPR, ..: 32 at a time, a lane's header each
   float L = -INFINITY, U = -INFINITY, sum = 0.f, x[PER] = {};
   for (int base = sub; base < nrec; base += 32 * WPR) {
@@ -860,29 +948,6 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
   const float f = sum == 0.f ? 0.f : ex2(U - L) / sum;
 #pragma unroll
   for (int k = 0; k < PER; ++k) out[k] = from_f<T>(x[k] * f);
-  if (WT && lane == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
-}
-
-// weights[b][g][j] += sum over the query rows of KV head g of their softmax weight of token j, from the
-// raw scores (log2 units) and each row's maximum and sum.  Thread per token of the unit's tiles.
-__global__ void __launch_bounds__(128) weights_kernel(Kv8Attn a) {
-  const int b = blockIdx.z, g = blockIdx.y;
-  wait_previous_kernel();
-  allow_next_kernel();
-  const Tiles ts = unit_tiles(a, b);
-  if (blockIdx.x >= ts.n) return;
-  const int j = ts.tile(blockIdx.x) * TILE + threadIdx.x, R = a.G * a.n;
-  if (j >= ts.len) return;
-  const size_t hd = (size_t)b * a.c.Hkv + g;
-  const float* s = a.scores + (hd * a.c.Lmax + j) * R;
-  const float2* st = (const float2*)a.stats + hd * R;
-  float w = 0.f;
-  for (int r = 0; r < R; ++r) {
-    const float2 x = st[r];
-    const float y = s[r];
-    if (y != -INFINITY) w += sm100::ex2(y - x.x) / x.y;
-  }
-  a.weights[hd * a.c.Lmax + j] += w;
 }
 
 // ============================================================================ eviction
@@ -942,8 +1007,8 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
   __shared__ __align__(8) int sTot[2];
   __shared__ int sWarp[2][SEL_WARPS], sPick[2];
   const int hd = blockIdx.x / CL, rank = blockIdx.x % CL, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  wait_previous_kernel();
   allow_next_kernel();
+  wait_previous_kernel();
   const int len = min(max(lens[b], 0), Lmax);
   const float* w = weights + (size_t)hd * Lmax;
   int* out = kept + (size_t)hd * keep;
@@ -1127,8 +1192,8 @@ __global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args 
   __shared__ float red[AP_THREADS / 32];
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
-  wait_previous_kernel();
   allow_next_kernel();
+  wait_previous_kernel();
   const int t0 = blockIdx.x * d.block, rows = min(d.block, lens2[b] - t0);
   if (rows <= 0) return;
   const size_t hd = (size_t)b * a.Hkv + g;
@@ -1242,7 +1307,7 @@ size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t
   *stats = o;
   if (weights) o += al((size_t)c.B * c.Hkv * R * 8);
   *scores = o;
-  if (weights) o += al((size_t)c.B * c.Hkv * c.Lmax * R * 4);
+  if (weights) o += al((size_t)c.B * c.Hkv * c.Lmax * nrg * RT * 4);
   return o;
 }
 
@@ -1264,10 +1329,9 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
     if ((e = launch_dependent(kernel, grid, kv8::AT_THREADS, smem, s, tk, tv, a, status)) != cudaSuccess) return e;
     // few ranges per unit: a warp per row
     const bool few = grid <= 8LL * a.c.B * a.c.Hkv * ((R + 8 * NT - 1) / (8 * NT));
-    e = launch_dependent(few ? kv8::merge_kernel<T, DH, WT, 1> : kv8::merge_kernel<T, DH, WT, 8>,
-                         dim3(few ? (R + 7) / 8 : R, a.c.Hkv, a.c.B), kv8::MG_THREADS, 0, s, a, 8 * NT, grid);
-    if (e != cudaSuccess || !WT) return e;
-    return launch_dependent(kv8::weights_kernel, dim3((a.c.Lmax + kv8::TILE - 1) / kv8::TILE, a.c.Hkv, a.c.B), 128, 0, s, a);
+    const int rows = few ? (R + 7) / 8 : R, tokens = WT ? (a.c.Lmax + kv8::WG_TILES * kv8::TILE - 1) / (kv8::WG_TILES * kv8::TILE) : 0;
+    return launch_dependent(few ? kv8::merge_kernel<T, DH, WT, 1> : kv8::merge_kernel<T, DH, WT, 8>,
+                            dim3(rows + tokens, a.c.Hkv, a.c.B), kv8::MG_THREADS, 0, s, a, 8 * NT, grid);
   };
   auto with_wt = [&](auto type, auto dh, auto nts) {
     return a.weights ? run(type, dh, nts, std::true_type()) : run(type, dh, nts, std::false_type());
