@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
 // barrier across warps in the loop, 16 KB per warp in flight.  The token order inside 16 rows
 // (slot_token) is chosen so that both kinds of fragment loads are free of bank conflicts.
 //
-// Work: the 128-token tiles that a unit's rows see, over all units in order, are cut into equal ranges,
-// one per CTA, so ragged batches stay balanced; a unit that falls into several ranges leaves partial
+// Work: the 128-token tiles that a unit's rows see, over all units in order, are cut into ranges of equal
+// length (give or take one tile), one per CTA, so ragged batches stay balanced; a unit that falls into several ranges leaves partial
 // results (slot = CTA + unit, which increases along the ranges and never repeats) for merge_kernel.
 constexpr int AT_THREADS = 128;
 constexpr int TILE = 128;      // tokens per CTA step, 32 per warp
@@ -280,6 +280,14 @@ __device__ __forceinline__ Tiles unit_tiles(const Kv8Attn& a, int b) {
   t.n = t.len > 0 ? t.nsk + (t.len - 1) / TILE - t.lo + 1 : 0;
   return t;
 }
+struct Split {  // `total` tiles over `grid` CTAs: the first `more` of them take one tile more than the others
+  long long base, more;
+  __device__ __forceinline__ Split(long long total, int grid) : base(total / grid), more(total % grid) {}
+  __device__ __forceinline__ long long start(long long cta) const { return cta * base + min(cta, more); }
+  __device__ __forceinline__ int cta_of(long long tile) const {
+    return (int)(tile < more * (base + 1) ? tile / (base + 1) : more + (tile - more * (base + 1)) / base);
+  }
+};
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -341,6 +349,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
   __shared__ float sStat[4][RT][3];  // ml, l, mu of each warp
   __shared__ long long sScan[AT_THREADS / 32];
   __shared__ int sStart[2];
+  __shared__ Tiles sTiles;
   __shared__ int sAbort;
   volatile int* abort = &sAbort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, c4 = lane & 3;
@@ -376,13 +385,17 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
       if (i < warp) before += sScan[i];
       total += sScan[i];
     }
-    const long long share = (total + gridDim.x - 1) / gridDim.x, w0 = share * blockIdx.x;
+    const long long w0 = Split(total, gridDim.x).start(blockIdx.x);
     if (w0 >= before && w0 < before + own) {  // one thread at most
       long long left = w0 - before;
       int b = b0;
       for (;; ++b) {
-        const long long t = (long long)unit_tiles(a, b).n * upb;
-        if (left < t) break;
+        const Tiles x = unit_tiles(a, b);
+        const long long t = (long long)x.n * upb;
+        if (left < t) {
+          sTiles = x;
+          break;
+        }
         left -= t;
       }
       sStart[0] = b;
@@ -390,11 +403,10 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
     }
     __syncthreads();
   }
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
-  const long long w0 = share * blockIdx.x, w1 = min(total, w0 + share);
-  if (w0 >= w1) return;
-  int todo = (int)(w1 - w0), b = sStart[0];
-  Tiles ts = unit_tiles(a, b);
+  const Split split(total, gridDim.x);
+  int todo = (int)(split.start(blockIdx.x + 1) - split.start(blockIdx.x)), b = sStart[0];
+  if (todo == 0) return;
+  Tiles ts = sTiles;
   int u = sStart[1] / ts.n, first = sStart[1] % ts.n;  // unit within the sequence, its first tile here
   int kvit = 0;  // tiles this warp has taken from its stages
   const uint64_t pol = policy_evict_first();  // the cache is read once
@@ -419,6 +431,17 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
       tma_load_2d_hint(mine + st * 2 * C::HALF, &tmK, &full[st], 0, y, pol);
       tma_load_2d_hint(mine + st * 2 * C::HALF + C::HALF, &tmV, &full[st], 0, y, pol);
     };
+    // the queries' loads go first: behind the first tiles they would wait for all of those (4 us at
+    // 131072 tokens, 36 MB in flight)
+    float qx[NT][KW / 4][16];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = min(rg * RT + t * 8 + g8, R - 1);
+      const T* qr = (const T*)a.q + ((size_t)b * a.n + r / a.G) * (size_t)(a.c.Hkv * a.G * DH) +
+                    (size_t)(g * a.G + r % a.G) * DH;
+#pragma unroll
+      for (int q = 0; q < KW / 4; ++q) load16<T>(qr + q * 64 + c4 * 16, qx[t][q]);
+    }
     if (lane == 0) {
       fence_proxy_async();  // (the stages held this warp's O of the segment before)
       for (int i = 0; i < STAGES && i < cnt; ++i) fetch(i, (kvit + i) % STAGES);
@@ -431,14 +454,11 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
     int qpos[NT][2];       // their positions; -1: not a row
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = rg * RT + t * 8 + g8;
-      const bool in = r < R;
-      const T* qr = (const T*)a.q + ((size_t)b * a.n + (in ? r / a.G : 0)) * (size_t)(a.c.Hkv * a.G * DH) +
-                    (size_t)(g * a.G + (in ? r % a.G : 0)) * DH;
-      float x[KW / 4][16], m = 0.f;
+      const bool in = rg * RT + t * 8 + g8 < R;
+      float(&x)[KW / 4][16] = qx[t];
+      float m = 0.f;
 #pragma unroll
       for (int q = 0; q < KW / 4; ++q) {
-        load16<T>(qr + q * 64 + c4 * 16, x[q]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (!in) x[q][i] = 0.f;
@@ -764,9 +784,11 @@ struct Records {
 };
 __device__ __forceinline__ Records unit_records(const Kv8Attn& a, int RT, int DH, int grid, long long before,
                                                 long long total, int b, int u, int upb, int tiles) {
-  const long long share = (total + grid - 1) / grid, start = before + (long long)u * tiles, end = start + tiles - 1;
-  const int c0 = (int)(start / share);
-  return {a.part + ((size_t)b * upb + u + c0) * RT * (DH + 4), (size_t)RT * (DH + 4), (int)(end / share) - c0 + 1};
+  const Split split(total, grid);
+  const long long start = before + (long long)u * tiles;
+  const int c0 = split.cta_of(start);
+  return {a.part + ((size_t)b * upb + u + c0) * RT * (DH + 4), (size_t)RT * (DH + 4),
+          split.cta_of(start + tiles - 1) - c0 + 1};
 }
 
 // weights[b][g][j] += sum over the query rows of KV head g of their softmax weight of token j, from the raw
@@ -906,7 +928,7 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
     for (int k = 0; k < PER; ++k) x[k] *= fu;
     const float f = h.z == -INFINITY ? 1.f : ex2(h.z - U);
     const int m = min(32, (nrec - base + WPR - 1) / WPR);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < m; ++k) {
       const float fk = __shfl_sync(0xffffffffu, f, k);
       const float* p = rec0 + (size_t)(base + k * WPR) * step + 4 + lane * PER;
@@ -1312,7 +1334,13 @@ size_t kv8_attention_scratch(const Kv8Args& c, int G, int n, int weights, size_t
 }
 
 cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream_t s) {
-  const int R = a.G * a.n, nt = kv8_groups(R), grid = kv8_grid(R, a.c.dh);
+  const int R = a.G * a.n, nt = kv8_groups(R), most = kv8_grid(R, a.c.dh);
+  const long long units = (long long)a.c.B * a.c.Hkv * ((R + 8 * nt - 1) / (8 * nt));
+  // Few ranges per unit: a warp joins a row.  Otherwise a CTA does, and the attention leaves a few CTAs'
+  // room free, so that those CTAs are in place and past their prologue when it ends (1 x 131072, 28/4
+  // heads: GRID_NOTE)
+  const bool few = most <= 8 * units;
+  const int grid = few ? most : most - (int)(R * units / 2 + 1 < most / 16 ? R * units / 2 + 1 : most / 16);
   const long long rows = (long long)a.c.B * a.c.Hkv * a.c.Lmax;
   CUtensorMap tk, tv;
   cudaError_t me = make_tmap_u8(&tk, a.c.k, rows, a.c.dh, 32);
@@ -1327,8 +1355,6 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(kernel, grid, kv8::AT_THREADS, smem, s, tk, tv, a, status)) != cudaSuccess) return e;
-    // few ranges per unit: a warp per row
-    const bool few = grid <= 8LL * a.c.B * a.c.Hkv * ((R + 8 * NT - 1) / (8 * NT));
     const int rows = few ? (R + 7) / 8 : R, tokens = WT ? (a.c.Lmax + kv8::WG_TILES * kv8::TILE - 1) / (kv8::WG_TILES * kv8::TILE) : 0;
     return launch_dependent(few ? kv8::merge_kernel<T, DH, WT, 1> : kv8::merge_kernel<T, DH, WT, 8>,
                             dim3(rows + tokens, a.c.Hkv, a.c.B), kv8::MG_THREADS, 0, s, a, 8 * NT, grid);
