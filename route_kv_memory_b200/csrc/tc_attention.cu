@@ -124,47 +124,68 @@ __device__ __forceinline__ int entry_token(int v, int S, int* slot) {
   return v >= 0 && t < S ? t : -1;
 }
 
-// MODE 2, padded batches: the items of rows in use only, sequence by sequence, longest pairs first, the
-// heads of a pair next to each other.  first[b]: the items in front of sequence b's (built per CTA from
-// lens; the static snake would otherwise give some CTAs mostly items behind the sequences' ends:
-// LENS_NOTE).
+// MODE 2 work items.  The query tiles of a (sequence, KV group) are numbered f = qt * G + (head of the
+// group), and an item takes tiles 2 P and 2 P + 1: mostly two heads of one query tile, which share their
+// list of key tiles, so that both halves of the ping-pong have a tile in every step (two query tiles of one
+// head, as in MODE 0, leave each half idle for a step of every window: WINDOW_PAIRS_NOTE).
+__host__ __device__ __forceinline__ int window_pairs(int rows, int G) { return ((rows + BQ - 1) / BQ * G + 1) / 2; }
+// Item w as its sequence, group and P.  Padded batches: the items of rows in use only, sequence by
+// sequence, longest first, with first[b] the items in front of sequence b's (built per CTA from lens; the
+// static snake would otherwise give some CTAs mostly items behind the sequences' ends: 2 x 4096 with
+// 1006 rows in use in the second, 28/4 heads, window 1024: 150 -> 95 us).
 constexpr int MAX_RAGGED = 512;  // sequences; more: every item is enumerated and the empty ones skipped
-__device__ __forceinline__ Work used_item(int w, const int* first, int B, int Hq) {
-  int lo = 0, hi = B;  // first[lo] <= w < first[hi]
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (first[m] <= w) lo = m;
-    else hi = m;
+struct GroupPair {
+  int b, g, P;
+};
+__device__ __forceinline__ GroupPair window_pair(int w, const AttnArgs& a, const int* first) {
+  GroupPair r;
+  if (first) {
+    int lo = 0, hi = a.B;  // first[lo] <= w < first[hi]
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (first[m] <= w) lo = m;
+      else hi = m;
+    }
+    const int back = first[lo + 1] - 1 - w;
+    r.b = lo;
+    r.P = back / a.Hkv;
+    r.g = back % a.Hkv;
+  } else {  // as work_item: chunks of streams
+    const int np = window_pairs(a.S, a.Hq / a.Hkv), NS = a.B * a.Hkv;
+    const int k = w / (a.chunk * np), cs = min(a.chunk, NS - k * a.chunk), rem = w - k * a.chunk * np;
+    const int st = k * a.chunk + rem % cs;
+    r.P = np - 1 - rem / cs;
+    r.b = st / a.Hkv;
+    r.g = st % a.Hkv;
   }
-  Work r;
-  r.b = lo;
-  r.pair = (first[lo + 1] - 1 - w) / Hq;
-  r.h = Hq - 1 - (first[lo + 1] - 1 - w) % Hq;
   return r;
 }
-// MODE 2 work item: query tiles 2 pair and 2 pair + 1 of head h of sequence b (len rows in use).
-// Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
+// The item's tiles t = 0, 1: query tile qt[t] of head h[t] (len rows in use; a last odd tile's partner lies
+// behind them).  Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
 struct WWork {
-  int b, h, pair, len, lo, nsk, n0, n1, s1;
+  int b, g, qt0, qt1, h0, h1, len, lo, nsk, n0, n1, s1;
   __device__ __forceinline__ int key_tile(int j) const { return j == 0 ? lo : (j <= nsk ? j - 1 : lo + j - nsk); }
 };
-__device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, int npairs, const int* first) {
-  const Work it = first ? used_item(w, first, a.B, a.Hq) : work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
+__device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, const int* first) {
+  const GroupPair it = window_pair(w, a, first);
+  const int G = a.Hq / a.Hkv;
   WWork r;
   r.b = it.b;
-  r.h = it.h;
-  r.pair = it.pair;
+  r.g = it.g;
+  r.qt0 = 2 * it.P / G;
+  r.qt1 = (2 * it.P + 1) / G;
+  r.h0 = it.g * G + 2 * it.P % G;
+  r.h1 = it.g * G + (2 * it.P + 1) % G;
   r.len = a.lens ? min(max(a.lens[it.b], 0), a.S) : a.S;
   r.n0 = r.n1 = r.s1 = r.lo = r.nsk = 0;
-  const int qt = 2 * it.pair;
-  if (qt * BQ >= r.len) return r;
+  if (r.qt0 * BQ >= r.len) return r;
   const int last = (r.len - 1) / BKV;
-  const int lo0 = a.window ? max(0, qt * BQ - a.window + 1) / BKV : 0;
-  const int lo1 = a.window ? max(0, (qt + 1) * BQ - a.window + 1) / BKV : 0;
-  const int hi1 = min(qt + 1, last);
+  const int lo0 = a.window ? max(0, r.qt0 * BQ - a.window + 1) / BKV : 0;
+  const int lo1 = a.window ? max(0, r.qt1 * BQ - a.window + 1) / BKV : 0;
+  const int hi1 = min(r.qt1, last);
   r.lo = lo0;
   r.nsk = min((a.sinks + BKV - 1) / BKV, lo0);
-  r.n0 = 1 + r.nsk + qt - lo0;
+  r.n0 = 1 + r.nsk + r.qt0 - lo0;
   r.n1 = 1 + r.nsk + hi1 - lo0;
   r.s1 = lo1 > lo0 && lo0 * BKV >= a.sinks && hi1 > lo0 ? 1 : 0;
   return r;
@@ -244,16 +265,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   const int nqt = (a.S + BQ - 1) / BQ;
   const int npairs = (nqt + 1) / 2;
+  const int G = a.Hq / a.Hkv;
   const int nbj = a.B * a.nblk;
-  int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : a.B * a.Hq * npairs;
-  const int* first = nullptr;  // MODE 2, padded batches: see used_item
+  int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : WN ? a.B * a.Hkv * window_pairs(a.S, G) : a.B * a.Hq * npairs;
+  const int* first = nullptr;  // MODE 2, padded batches: see window_pair
   if constexpr (WN) {
     if (a.lens && a.B <= MAX_RAGGED) {
       int* sfirst = (int*)(smem + 2 * C::Q_BYTES + 2 * C::KV_BYTES + 256);
       if (warp == 0) {  // prefix sums of the sequences' items, 32 at a time
         int sum = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-          const int b = b0 + lane, n = b < a.B ? (min(max(a.lens[b], 0), a.S) + 2 * BQ - 1) / (2 * BQ) * a.Hq : 0;
+          const int b = b0 + lane, n = b < a.B ? window_pairs(min(max(a.lens[b], 0), a.S), G) * a.Hkv : 0;
           int inc = n;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -270,7 +292,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       nwork = sfirst[a.B];
     }
   }
-  const int G = a.Hq / a.Hkv;
   const int RPT = gathered_rows_per_token(G);  // MODE 1: tile rows per token (its G heads first)
   const int tpt = BQ / RPT;                    // MODE 1: tokens per query tile
   const long long q_rows_per_b = a.q_bstride / a.q_ld;
@@ -399,9 +420,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Work it;
         WWork ww;
         if constexpr (WN) {
-          ww = window_item(w, a, npairs, first);
+          ww = window_item(w, a, first);
           if (ww.n1 == 0) continue;  // (every role skips the same items)
-          it = {ww.b, ww.h, ww.pair};
+          it = {ww.b, ww.h0, 0};
         } else {
           it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
         }
@@ -414,9 +435,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             break;
           }
           mbar_expect_tx(&q_full[t], C::Q_BYTES);
-          const int qy = (int)(it.b * q_rows_per_b) + (2 * it.pair + t) * BQ;
+          const int qy = (int)(it.b * q_rows_per_b) + (WN ? (t ? ww.qt1 : ww.qt0) : 2 * it.pair + t) * BQ;
+          const int qx = (WN && t ? ww.h1 : it.h) * DH;
           for (int hb = 0; hb < NH; ++hb)
-            tma_load_2d_hint(sQ + t * C::Q_BYTES + hb * C::HALF, &tmQ, &q_full[t], it.h * DH + hb * 64, qy, pol_once);
+            tma_load_2d_hint(sQ + t * C::Q_BYTES + hb * C::HALF, &tmQ, &q_full[t], qx + hb * 64, qy, pol_once);
         }
         if (!qok) break;
         const int nkv = WN ? ww.n1 : 2 * it.pair + 2;
@@ -491,7 +513,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       if constexpr (WN) {
-        ww = window_item(w, a, npairs, first);
+        ww = window_item(w, a, first);
         if (ww.n1 == 0) continue;
         nx0 = ww.n0;
         nx1 = ww.n1;
@@ -595,7 +617,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       WWork ww;
       int j0 = 0;  // first step of this tile
       if constexpr (WN) {
-        ww = window_item(w, a, npairs, first);
+        ww = window_item(w, a, first);
         if (ww.n1 == 0) continue;
       }
       const int wi = done++;
@@ -616,8 +638,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         masked = __any_sync(0xffffffffu, row_lim != kNoMask);
       } else if constexpr (WN) {
         b = ww.b;
-        h = ww.h;
-        row = (2 * ww.pair + t) * BQ + r;
+        h = t ? ww.h1 : ww.h0;
+        row = (t ? ww.qt1 : ww.qt0) * BQ + r;
         j0 = t ? ww.s1 : 0;
         nkv = t ? ww.n1 : ww.n0;
         row_lim = row;
@@ -871,7 +893,7 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
     return cudaErrorInvalidValue;
   // MODE 1: the item count is on the device (block_lists); idle CTAs leave at once
   const int nqt = (a.S + tca::BQ - 1) / tca::BQ;
-  const int nwork = a.B * a.Hq * ((nqt + 1) / 2);
+  const int nwork = win ? a.B * a.Hkv * tca::window_pairs(a.S, a.Hq / a.Hkv) : a.B * a.Hq * ((nqt + 1) / 2);
   const int grid = ga ? sms : (nwork < sms ? nwork : sms);
   // causal mode: streams per chunk of the work order.  When the K/V of all streams fits in half of
   // L2, one chunk of all streams; otherwise the fewest streams for which one round of `grid` items
