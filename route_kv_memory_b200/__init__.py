@@ -264,11 +264,6 @@ def mka_decode_step(c: mka_config, packed, state, max_positions: int, x_new, out
 
 
 # ------------------------------------------------------------------ bounded-memory attention
-def _dtype(t: torch.Tensor, want: torch.dtype, name: str) -> None:
-    if t.dtype != want:
-        raise ValueError(f"{name} must be {want}, not {t.dtype}")
-
-
 def _call_stream(tensors, stream, *caches):
     """The stream pointer of a call on `tensors` (and 8-bit caches): they must live on the current device, and
     a stream other than the current one is recorded on them."""
@@ -300,12 +295,20 @@ def _dense(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, *shape: int
     return t.data_ptr()
 
 
+def _positions(t: Optional[torch.Tensor], name: str, B: int):
+    """Pointer of one int32 per sequence (None passes)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be {B} contiguous int32, not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
 def _row_stride(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, S: int, heads: int, dh: int) -> int:
     """Row stride of t [B, S, heads, dh] or [B, S, heads * dh] (see mka_attn_strides)."""
-    _dtype(t, dtype, name)
-    width = heads * dh
-    if t.shape != (B, S, heads, dh) and t.shape != (B, S, width):
-        raise ValueError(f"{name} must be [{B}, {S}, {heads}, {dh}] or [{B}, {S}, {width}], not {tuple(t.shape)}")
+    width, shape = heads * dh, t.shape
+    if t.dtype is not dtype or (shape != (B, S, heads, dh) and shape != (B, S, width)):
+        raise ValueError(f"{name} must be {dtype} [{B}, {S}, {heads}, {dh}] or [{B}, {S}, {width}], not {t.dtype} {tuple(shape)}")
     if t.is_contiguous():
         return width
     st = t.stride()
@@ -339,7 +342,7 @@ def mka_window_attention(c: mka_attn_config, q, k, v, lens, out, lse=None, strea
     st = mka_attn_strides(_row_stride(q, "q", bf, B, S, H, d), _row_stride(k, "k", bf, B, S, G, d),
                           _row_stride(v, "v", bf, B, S, G, d), _row_stride(out, "out", bf, B, S, H, d), 0)
     _check(_lib.mka_window_attention(c, st, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                     _dense(lens, "lens", torch.int32, B), out.data_ptr(), _lse_ptr(c, lse), s),
+                                     _positions(lens, "lens", B), out.data_ptr(), _lse_ptr(c, lse), s),
            "mka_window_attention")
 
 
@@ -356,7 +359,7 @@ def mka_window_attention_backward(c: mka_attn_config, q, k, v, out, lse, dout, l
                           _row_stride(dout, "dout", bf, B, S, H, d))
     _check(_lib.mka_window_attention_backward(
         c, st, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _lse_ptr(c, lse), dout.data_ptr(),
-        _dense(lens, "lens", torch.int32, B), _dense(dq, "dq", bf, B, S, H * d), _dense(dk, "dk", bf, B, S, G * d),
+        _positions(lens, "lens", B), _dense(dq, "dq", bf, B, S, H * d), _dense(dk, "dk", bf, B, S, G * d),
         _dense(dv, "dv", bf, B, S, G * d), ws.data_ptr(), ws.numel() * ws.element_size(), s),
         "mka_window_attention_backward")
 
@@ -396,7 +399,9 @@ def _check_cache(c: mka_kv8_config, x: mka_kv8_cache) -> None:
 
 def _kv_rows(c: mka_kv8_config, t: torch.Tensor, name: str):
     """(rows, row stride, batch stride) of K/V rows [B, n, Hkv, dh] or [B, n, Hkv * dh]."""
-    _dtype(t, torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32, name)
+    want = torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32
+    if t.dtype is not want:
+        raise ValueError(f"{name} must be {want}, not {t.dtype}")
     B, H, d, shape, st = c.batch, c.n_kv_heads, c.d_head, t.shape, t.stride()
     n = shape[1] if len(shape) > 2 else -1
     if shape == (B, n, H, d):
@@ -424,7 +429,7 @@ def mka_kv8_append(c: mka_kv8_config, cache: mka_kv8_cache, k_new, v_new, pos, c
     _check_cache(c, cache)
     rows = _kv_pair(c, k_new, v_new, ("k_new", "v_new"))
     _check(_lib.mka_kv8_append(c, cache, k_new.data_ptr(), v_new.data_ptr(), rows[1], rows[2], rows[0],
-                               _dense(pos, "pos", torch.int32, c.batch), _dense(count, "count", torch.int32, c.batch), s),
+                               _positions(pos, "pos", c.batch), _positions(count, "count", c.batch), s),
            "mka_kv8_append")
 
 
@@ -433,8 +438,8 @@ def mka_kv8_read(c: mka_kv8_config, cache: mka_kv8_cache, first, rows, k_out, v_
     s = _call_stream((first, rows, k_out, v_out), stream, cache)
     _check_cache(c, cache)
     at = _kv_pair(c, k_out, v_out, ("k_out", "v_out"))
-    _check(_lib.mka_kv8_read(c, cache, _dense(first, "first", torch.int32, c.batch),
-                             _dense(rows, "rows", torch.int32, c.batch), at[0], k_out.data_ptr(), v_out.data_ptr(), at[1],
+    _check(_lib.mka_kv8_read(c, cache, _positions(first, "first", c.batch),
+                             _positions(rows, "rows", c.batch), at[0], k_out.data_ptr(), v_out.data_ptr(), at[1],
                              at[2], s), "mka_kv8_read")
 
 
@@ -450,7 +455,7 @@ def mka_kv8_attention(c: mka_kv8_config, cache: mka_kv8_cache, q, lens, out, wei
     dt = torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32
     n = q.shape[1] if q.dim() >= 2 else 0
     _check(_lib.mka_kv8_attention(
-        c, cache, _dense(q, "q", dt, c.batch, n, c.n_q_heads * c.d_head), n, _dense(lens, "lens", torch.int32, c.batch),
+        c, cache, _dense(q, "q", dt, c.batch, n, c.n_q_heads * c.d_head), n, _positions(lens, "lens", c.batch),
         _dense(out, "out", dt, c.batch, n, c.n_q_heads * c.d_head),
         _dense(weights, "weights", torch.float32, c.batch, c.n_kv_heads, c.max_positions), ws.data_ptr(),
         ws.numel() * ws.element_size(), s), "mka_kv8_attention")
@@ -468,8 +473,8 @@ def mka_kv8_evict(c: mka_kv8_config, cache: mka_kv8_cache, lens, weights, keep: 
     _check_cache(dst_c, dst)
     B, H = c.batch, c.n_kv_heads
     _check(_lib.mka_kv8_evict(
-        c, cache, _dense(lens, "lens", torch.int32, B), _dense(weights, "weights", torch.float32, B, H, c.max_positions),
-        keep, first, recent, dst_c, dst, _dense(dst_lens, "dst_lens", torch.int32, B),
+        c, cache, _positions(lens, "lens", B), _dense(weights, "weights", torch.float32, B, H, c.max_positions),
+        keep, first, recent, dst_c, dst, _positions(dst_lens, "dst_lens", B),
         _dense(dst_weights, "dst_weights", torch.float32, B, H, dst_c.max_positions),
         _dense(kept, "kept", torch.int32, B, H, keep), ws.data_ptr(), ws.numel() * ws.element_size(), s), "mka_kv8_evict")
 

@@ -987,7 +987,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // forced tokens, keys above the found one, and of those equal to it the first `need` in position order --
 // and after a prefix sum over lanes, warps and CTAs writes it in order.  Keys are loaded coalesced and
 // turned to their owners through shared memory; a lane's matches are bits of one word, so that a token
-// costs a few instructions a pass (SELECT_NOTE).
+// costs a few instructions a pass.
 constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32, SEL_BINS = 2048, SEL_CLUSTER = 8;
 constexpr int KPT = 16;                     // positions per lane and round
 constexpr int SEL_ROUND = SEL_THREADS * KPT;
@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
   extern __shared__ uint32_t skeys[];
   __shared__ __align__(8) int hist[SEL_BINS], all[SEL_BINS];  // this CTA's counts, the cluster's
   __shared__ __align__(8) int sTot[2];
-  __shared__ int sWarp[2][SEL_WARPS], sPick[2];
+  __shared__ int sWarp[2][SEL_WARPS], sPick[3];
   const int hd = blockIdx.x / CL, rank = blockIdx.x % CL, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   allow_next_kernel();
   wait_previous_kernel();
@@ -1066,6 +1066,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
   if (once) load(0);
   int need = keep - first - recent;  // of the middle tokens; fewer than there are
   const bool none = need == 0;
+  int low = 0;
   uint32_t prefix = 0, match = 0;  // match (once): this lane's middle positions that match the digits so far
   for (int pass = 0; pass < 3 && !none; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
@@ -1120,12 +1121,16 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
       const bool second = need > before + c.y;
       sPick[0] = second ? d - 1 : d;
       sPick[1] = need - before - (second ? c.y : 0);
+      sPick[2] = second ? c.x : c.y;
     }
     __syncthreads();
     prefix = prefix << bits | (uint32_t)sPick[0];
     need = sPick[1];
+    low = shift;
+    if (need == sPick[2]) break;  // all of the bin is kept: the digits below do not matter
   }
-  // prefix: the key of the last kept middle token; need: how many with exactly that key.  A lane's sure
+  // prefix: the upper bits (above `low`) of the key of the last kept middle token, mostly 22 of them; need:
+  // how many with exactly those.  A lane's sure
   // positions (forced, or above the key) and tied ones as bits, and their counts before it in its warp
   auto bits_of = [&](int p, uint32_t& sure, uint32_t& tie) {
     const uint32_t in = bit_range(0, ce - p), mid = bit_range(m0 - p, min(m1, ce) - p);
@@ -1133,7 +1138,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
     if (!none) {
 #pragma unroll
       for (int j = 0; j < KPT; ++j) {
-        const uint32_t k = own[j];
+        const uint32_t k = own[j] >> low;
         above |= k > prefix ? 1u << j : 0u;
         equal |= k == prefix ? 1u << j : 0u;
       }
