@@ -220,6 +220,13 @@ MKA_API int mka_prefill_backward(const mka_config* cfg, const void* packed, cons
                                  const void* dout, void* dx, float* dw_q, float* dw_k, float* dw_v, float* dw_r1,
                                  float* dw_r2, float* dlambda_out, void* ws, size_t ws_bytes, void* stream);
 
+/* The fused K/V cache inside a decode state (host function, no device work): *k and *v receive the device
+ * addresses of [B, max_positions, Hkv*dh] (dtype) arrays whose first rows, up to the state's position,
+ * hold the fused K and V, for operators that read or convert them (mka_kv8_append).  They are valid as
+ * long as `state` is; only the library's own calls write them. */
+MKA_API int mka_state_kv(const mka_config* cfg, int32_t max_positions, const void* state, size_t state_bytes,
+                         const void** k, const void** v);
+
 /* One decode step for the next token of each sequence (notes §3: the cache holds the
  * fused routed K/V).  x_new [B, d] (dtype) -> out [B, Hq*dh] (dtype).  Runs the
  * router, reads M2 and recalls from the finished blocks, appends the fused K/V row

@@ -46,7 +46,7 @@ EXPORTED = [
     "mka_prefill_backward", "mka_set_wait_limit", "mka_window_attention",
     "mka_window_attention_backward_workspace_size", "mka_window_attention_backward",
     "mka_kv8_append", "mka_kv8_read", "mka_kv8_attention_workspace_size", "mka_kv8_attention",
-    "mka_kv8_evict_workspace_size", "mka_kv8_evict",
+    "mka_kv8_evict_workspace_size", "mka_kv8_evict", "mka_state_kv",
 ]
 
 
@@ -121,6 +121,7 @@ _SIGS = {
     "mka_kv8_attention_workspace_size": (_sz, [_kcp, _i32, _i32]),
     "mka_kv8_attention": (ctypes.c_int, [_kcp, _kvp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mka_kv8_evict_workspace_size": (_sz, [_kcp, _i32]),
+    "mka_state_kv": (ctypes.c_int, [_cfgp, _i32, _vp, _sz, ctypes.POINTER(_vp), ctypes.POINTER(_vp)]),
     "mka_kv8_evict": (ctypes.c_int, [_kcp, _kvp, _vp, _vp, _i32, _i32, _i32, _kcp, _kvp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -572,6 +573,19 @@ class FastMKALayer:
         mka_state_init(c, max_positions, st, stream)
         return st
 
+    def fused_kv(self, state: torch.Tensor, max_positions: int, batch: Optional[int] = None):
+        """The fused K and V inside a decode state, as views [B, max_positions, Hkv, d_head] of it (read only):
+        the rows up to the state's position are in use."""
+        c = make_config(self.cfg, batch=batch)
+        k, v = ctypes.c_void_p(), ctypes.c_void_p()
+        _check(_lib.mka_state_kv(ctypes.byref(c), max_positions, _ptr(state), state.numel() * state.element_size(),
+                                 ctypes.byref(k), ctypes.byref(v)), "mka_state_kv")
+        dt = torch.float32 if c.dtype == MKA_F32 else torch.bfloat16
+        n = c.batch * max_positions * c.n_kv_heads * c.d_head * dt.itemsize
+        raw = state.view(torch.uint8).view(-1)
+        return tuple(raw[p.value - state.data_ptr():][:n].view(dt).view(c.batch, max_positions, c.n_kv_heads, c.d_head)
+                     for p in (k, v))
+
     def decode(self, state, max_positions: int, x_new, out, stream=None) -> torch.Tensor:
         c = make_config(self.cfg, seq=1, batch=x_new.shape[0])
         key = ("decode", c.batch, max_positions)
@@ -579,3 +593,64 @@ class FastMKALayer:
             self._ws[key] = buffer(mka_decode_workspace_size(c, max_positions), self.device)
         mka_decode_step(c, self.packed, state, max_positions, x_new, out, self._ws[key], stream)
         return out
+
+
+class KV8Cache:
+    """Convenience owner of an 8-bit K/V cache: codes, scales, the positions in use (`lens`, on the device), and
+    with weights=True every position's summed attention weight.
+
+    Allocation happens here; every computation goes through the C ABI.  The calls of one cache share its scratch:
+    issue them on one stream, or ordered, and do not replay graphs captured from one cache at the same time.
+    """
+
+    def __init__(self, batch: int, max_positions: int, n_q_heads: int, n_kv_heads: int, d_head: int, block: int = 64,
+                 dtype: str = "bf16", window: int = 0, sinks: int = 0, attn_scale: Optional[float] = None,
+                 weights: bool = False, device="cuda"):
+        self.c = make_kv8_config(batch, max_positions, n_q_heads, n_kv_heads, d_head, block, dtype, window, sinks,
+                                 attn_scale)
+        if mka_kv8_attention_workspace_size(self.c, 1) == 0:  # a configuration the library refuses, with its reason
+            raise MKAError(MKA_ERR_INVALID_ARG, "KV8Cache")
+        codes = [torch.zeros(batch, n_kv_heads, max_positions, d_head, dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.ones(batch, n_kv_heads, -(-max_positions // block), device=device) for _ in "kv"]
+        self.cache = kv8_cache(*codes, *scales)
+        self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.weights = torch.zeros(batch, n_kv_heads, max_positions, device=device) if weights else None
+        self._ws = {}
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, count: Optional[torch.Tensor] = None) -> None:
+        """Rows [B, n, Hkv, d_head] behind the positions in use, count[b] (None: all) of them.  A sequence that they
+        do not fit keeps what it has (mka_status() then says MKA_ERR_CAPACITY)."""
+        mka_kv8_append(self.c, self.cache, k, v, self.lens, count)
+        after = self.lens + (k.shape[1] if count is None else count.clamp(0, k.shape[1]))
+        self.lens.copy_(torch.where(after <= self.c.max_positions, after, self.lens))
+
+    def attend(self, q: torch.Tensor, out: torch.Tensor) -> torch.Tensor:
+        """Attention of the last n positions (their K/V appended before): q, out [B, n, Hq, d_head]."""
+        n = q.shape[1]
+        if n not in self._ws:
+            self._ws[n] = buffer(mka_kv8_attention_workspace_size(self.c, n, self.weights is not None), q.device)
+        mka_kv8_attention(self.c, self.cache, q, self.lens, out, self.weights, self._ws[n])
+        return out
+
+    def read(self, n: int):
+        """Values of the first n positions, [B, n, Hkv, d_head] each (rows past a sequence's end are 0)."""
+        dt = torch.float32 if self.c.dtype == MKA_F32 else torch.bfloat16
+        k, v = (torch.zeros(self.c.batch, n, self.c.n_kv_heads, self.c.d_head, dtype=dt, device=self.lens.device)
+                for _ in "kv")
+        mka_kv8_read(self.c, self.cache, None, self.lens, k, v)
+        return k, v
+
+    def evict(self, keep: int, first: int, recent: int, max_positions: int):
+        """Another cache of max_positions that holds, per sequence and KV head, the first, the last `recent` and
+        the heaviest of the positions, `keep` in all, with their weights.  Returns it and the kept positions
+        [B, Hkv, keep] (-1 past a sequence's last)."""
+        if self.weights is None:
+            raise ValueError("eviction goes by the weights: make the cache with weights=True")
+        c = self.c
+        new = KV8Cache(c.batch, max_positions, c.n_q_heads, c.n_kv_heads, c.d_head, c.block,
+                       "f32" if c.dtype == MKA_F32 else "bf16", c.window, c.sinks, c.attn_scale, True, self.lens.device)
+        kept = torch.empty(c.batch, c.n_kv_heads, keep, dtype=torch.int32, device=self.lens.device)
+        ws = buffer(mka_kv8_evict_workspace_size(c, keep), self.lens.device)
+        mka_kv8_evict(c, self.cache, self.lens, self.weights, keep, first, recent, new.c, new.cache, new.lens, new.weights,
+                      kept, ws)
+        return new, kept

@@ -416,6 +416,21 @@ size_t mka_state_size(const mka_config* cfg, int32_t max_positions) {
   return state_layout(d, max_positions).total;
 }
 
+int mka_state_kv(const mka_config* cfg, int32_t max_positions, const void* state, size_t state_bytes, const void** k,
+                 const void** v) {
+  Dims d;
+  int rc = check_cfg(cfg, &d);
+  if (rc != MKA_OK) return rc;
+  if (!state || !k || !v) return fail(MKA_ERR_INVALID_ARG, "mka_state_kv: NULL argument");
+  if (!aligned16(state)) return fail(MKA_ERR_INVALID_ARG, "mka_state_kv: state is not 16-byte aligned");
+  if (max_positions < 1) return fail(MKA_ERR_INVALID_ARG, "max_positions must be >= 1");
+  const StateLayout L = state_layout(d, max_positions);
+  if (state_bytes < L.total) return fail(MKA_ERR_WORKSPACE, "state holds %zu bytes, needs %zu", state_bytes, L.total);
+  *k = (const char*)state + L.kc;
+  *v = (const char*)state + L.vc;
+  return MKA_OK;
+}
+
 size_t mka_decode_workspace_size(const mka_config* cfg, int32_t max_positions) {
   Dims d;
   if (check_cfg(cfg, &d) != MKA_OK || max_positions < 1) return 0;

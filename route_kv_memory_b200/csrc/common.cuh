@@ -135,6 +135,12 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads
   return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
+// Raise a kernel's dynamic shared memory limit (no stream operation: allowed while capturing).
+template <typename F>
+inline cudaError_t raise_max_smem(F* func, size_t bytes) {
+  return cudaFuncSetAttribute((const void*)func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 // Raise a kernel's dynamic shared memory limit.  Skipped while `s` is being
 // captured into a CUDA graph: the attribute persists, and an eager call made
 // before the capture has already set it.

@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
 
     // join the four warps, each one's O in its own stages (none of its copies is in flight)
     float* so = (float*)mine;
-    if (!*abort) {
+    if (!__any_sync(0xffffffffu, *abort)) {  // (one answer for the warp: shuffles follow)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
             *(float2*)&so[r * OLD + g8 * (DH / 8) + 2 * m] = make_float2(o[m][t][i], o[m][t][i + 2]);
         }
     }
-    __syncthreads();
+    __syncthreads();  // (no wait follows in the segment: every thread sees the same abort)
     if (*abort) break;
     const bool whole = first == 0 && cnt == ts.n;
     const size_t slot = (size_t)blockIdx.x + (size_t)b * upb + u;
@@ -1357,7 +1357,7 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
     constexpr bool WT = decltype(wt)::value;
     auto* kernel = kv8::attention_kernel<T, DH, NT, WT>;
     constexpr int smem = kv8::AtCfg<DH>::SMEM;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = raise_max_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(kernel, grid, kv8::AT_THREADS, smem, s, tk, tv, a, status)) != cudaSuccess) return e;
     const int rows = few ? (R + 7) / 8 : R, tokens = WT ? (a.c.Lmax + kv8::WG_TILES * kv8::TILE - 1) / (kv8::WG_TILES * kv8::TILE) : 0;
@@ -1385,7 +1385,7 @@ cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, i
   int dev = 0, sms = 148, cl = 1;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   while (cl < kv8::SEL_CLUSTER && cl * 4096 < a.Lmax && cl * a.B * a.Hkv <= sms) cl *= 2;
-  cudaError_t e = cudaFuncSetAttribute(kv8::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kv8::SEL_SMEM);
+  cudaError_t e = raise_max_smem(kv8::select_kernel, kv8::SEL_SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2] = {};
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -846,7 +846,8 @@ cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
                         int* status, int grid, cudaStream_t s) {
   constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES
                                           : MODE == 2 ? (tca::MAX_RAGGED + 4) * 4 : 0);
-  cudaError_t e = set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
+  cudaError_t e = MODE == 2 ? raise_max_smem(tca::attn_tc_kernel<DH, MODE>, sm)
+                            : set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
   if (e != cudaSuccess) return e;
   if (MODE == 2) return launch_dependent(tca::attn_tc_kernel<DH, MODE>, grid, tca::NTHREADS, sm, s, tq, tk, tv, a, status);
   tca::attn_tc_kernel<DH, MODE><<<grid, tca::NTHREADS, sm, s>>>(tq, tk, tv, a, status);

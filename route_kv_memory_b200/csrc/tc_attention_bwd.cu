@@ -1067,11 +1067,12 @@ static cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tdo, con
                               const CUtensorMap& tv, const AttnBwdArgs& a, int* status, int sms, cudaStream_t s) {
   using C = tcb::Cfg<DH>;
   const int nqt = (a.S + tcb::BT - 1) / tcb::BT;
-  cudaError_t e = set_max_smem(tcb::attn_bwd_dkdv_kernel<DH, WN>, C::SMEM_DKDV, s);
+  cudaError_t e = WN ? raise_max_smem(tcb::attn_bwd_dkdv_kernel<DH, WN>, C::SMEM_DKDV)
+                     : set_max_smem(tcb::attn_bwd_dkdv_kernel<DH, WN>, C::SMEM_DKDV, s);
   if (e != cudaSuccess) return e;
   const int nkv = a.B * a.Hkv * (nqt + (WN ? a.sink_tiles * a.far_chunks : 0)), nq = a.B * a.Hq * nqt;
-  if ((e = set_max_smem(tcb::attn_bwd_dq_kernel<DH, WN>, C::SMEM_DQ, s)) != cudaSuccess) return e;
   if (WN) {
+    if ((e = raise_max_smem(tcb::attn_bwd_dq_kernel<DH, WN>, C::SMEM_DQ)) != cudaSuccess) return e;
     e = launch_dependent(tcb::attn_bwd_dkdv_kernel<DH, WN>, nkv < sms ? nkv : sms, tcb::NTHREADS, C::SMEM_DKDV, s, tq, tdo,
                          tk, tv, a, status);
     if (e != cudaSuccess) return e;
@@ -1080,6 +1081,7 @@ static cudaError_t launch_bwd(const CUtensorMap& tq, const CUtensorMap& tdo, con
   }
   tcb::attn_bwd_dkdv_kernel<DH, WN><<<nkv < sms ? nkv : sms, tcb::NTHREADS, C::SMEM_DKDV, s>>>(tq, tdo, tk, tv, a, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = set_max_smem(tcb::attn_bwd_dq_kernel<DH, WN>, C::SMEM_DQ, s)) != cudaSuccess) return e;
   tcb::attn_bwd_dq_kernel<DH, WN><<<nq < sms ? nq : sms, tcb::NTHREADS, C::SMEM_DQ, s>>>(tq, tdo, tk, tv, a, status);
   return cudaGetLastError();
 }

@@ -217,6 +217,9 @@ ATTN = [
     (2, 900, 4, 4, 64, 64, "bf16", 257, 140, 8, [900, 410]),
     (5, 260, 16, 2, 64, 16, "bf16", 0, 0, 1, [0, 260, 1, 17, 128]),
     (1, 2100, 6, 3, 128, 128, "bf16", 0, 0, 1, [2100]),
+    (1, 300, 28, 4, 128, 64, "bf16", 0, 0, 20, [300]),    # 140 query rows per KV head
+    (2, 200, 20, 1, 64, 32, "f32", 64, 2, 1, [200, 150]),  # 20 query heads on one KV head
+    (150, 70, 2, 1, 64, 16, "bf16", 0, 0, 1, [(7 * i) % 71 for i in range(150)]),  # more sequences than threads
 ]
 
 

@@ -104,6 +104,15 @@ def test_padded_batch(mka, case, lens):
 
 
 @pytest.mark.gpu
+def test_many_short_sequences(mka):
+    """More sequences than the forward keeps a table of, most of them shorter than the padding."""
+    B, S = 530, 150
+    x = draw(B, S, 2, 1, 64, 6)
+    lens = [(37 * b) % (S + 1) for b in range(B)]
+    check(run(mka, *x, 40, 2, lens), *x, 40, 2, lens)
+
+
+@pytest.mark.gpu
 def test_sequence_end_does_not_read_the_next_sequence(mka):
     """S is not a multiple of a tile: the tile's last rows belong to the next sequence, here all NaN there."""
     x = draw(2, 200, 2, 1, 64, 5)
