@@ -26,13 +26,16 @@
 // over the block's key tiles (the causal mask only for the block's own tokens) and leaves O / l
 // in bf16 with its log2 normaliser for the merge.
 //
-// MODE 2 (window with sinks): causal attention in which position t sees the last `window` positions
+// MODE 2, 3 (window with sinks): causal attention in which position t sees the last `window` positions
 // and the first `sinks` ones, over lens[b] rows of sequence b.  An item streams only the key tiles
 // that some row of its two query tiles sees: first the tile lo holding tile 0's oldest window key
 // (read by tile 0 alone when tile 1's window starts behind it and it holds no sink), then the sink
 // tiles before lo, then lo + 1 up to the diagonal; the order of keys does not matter to the softmax.
 // Only tiles crossed by the diagonal, the window's edge or the sinks' end are masked.  V rows at or
-// past lens[b] are cleared in shared memory before P V: their P is 0, but 0 * NaN is not.
+// past lens[b] are cleared in shared memory before P V: their P is 0, but 0 * NaN is not.  Bound, like
+// MODE 0, by the softmax (its exponentials and its round trips to the MMA warp), and with short windows
+// by the start and end of each item (about 10 us of its time): 1 x 32768, 32/8 heads, window 4096, 4
+// sinks: 2010 us = 1026 TFLOP/s of the seen pairs; window 1024: 775 us = 700 TFLOP/s.
 #include <cudaTypedefs.h>
 
 #include "kernels.h"
@@ -127,7 +130,7 @@ __device__ __forceinline__ int entry_token(int v, int S, int* slot) {
 // MODE 2 work items.  The query tiles of a (sequence, KV group) are numbered f = qt * G + (head of the
 // group), and an item takes tiles 2 P and 2 P + 1: mostly two heads of one query tile, which share their
 // list of key tiles, so that both halves of the ping-pong have a tile in every step (two query tiles of one
-// head, as in MODE 0, leave each half idle for a step of every window: WINDOW_PAIRS_NOTE).
+// head, as in MODE 0, leave each half idle for a step of every window; 1 x 32768, 32/8 heads, window 1024: 924 -> 840 us).
 __host__ __device__ __forceinline__ int window_pairs(int rows, int G) { return ((rows + BQ - 1) / BQ * G + 1) / 2; }
 // Item w as its sequence, group and P.  Padded batches: the items of rows in use only, sequence by
 // sequence, longest first, with first[b] the items in front of sequence b's (built per CTA from lens; the
@@ -201,8 +204,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 
-// MODE 0: causal attention; MODE 1: block-gathered rows; MODE 2: window with sinks (see the top of
-// the file).
+// MODE 0: causal attention; MODE 1: block-gathered rows; MODE 2, 3: window with sinks (see the top of
+// the file), 3 with the masked steps of the softmax in a path of their own.
 template <int DH, int MODE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  constexpr bool GA = MODE == 1, WN = MODE == 2;
+  constexpr bool GA = MODE == 1, WN = MODE >= 2, SPLIT = MODE == 3;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
@@ -666,13 +669,92 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if constexpr (WN) {
           const int k0 = ww.key_tile(j) * BKV, t0 = row - lane;  // t0: the warp's first row
           diag = k0 + BKV - 1 > t0 || (a.window && k0 <= t0 + 31 - a.window && k0 + BKV > a.sinks);
-          if (diag) {
+          if (!SPLIT && diag) {
             const int hi = row + 1 - k0, lo = a.window ? hi - a.window : 0, sk = a.sinks - k0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               see[c] = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
           }
         }
+        if (SPLIT && diag) {
+          // a masked step, apart from the others so that those stay free of masks: by chunks of 32 keys, of
+          // which the ones that no row of the warp sees are skipped
+          const int k0 = ww.key_tile(j) * BKV, hi = row + 1 - k0, lo = a.window ? hi - a.window : 0, sk = a.sinks - k0;
+          // bit e: this row sees key 32 c + e of the tile
+          auto word = [&](int c) { return low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c)); };
+          uint32_t some = 0;  // bit c: some row of the warp sees some of chunk c
+#pragma unroll
+          for (int c = 0; c < 4; ++c) some |= __any_sync(0xffffffffu, word(c) != 0) ? 1u << c : 0u;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (!(some & (1u << c))) continue;
+            uint32_t v[32];
+            tmem_ld32(s_tmem + c * 32, v);
+            const uint32_t see = word(c);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((see >> e) & 1) mx = fmaxf(mx, __uint_as_float(v[e]));
+          }
+          mx *= sl2;
+          float corr = 1.f;
+          bool rescale = false;
+          if (mx > m_ref + RESCALE_THRESHOLD) {
+            rescale = m_ref != -INFINITY;
+            corr = rescale ? ex2(m_ref - mx) : 0.f;
+            m_ref = mx;
+            l *= corr;
+          }
+          if (__ballot_sync(0xffffffffu, rescale)) {  // as below
+            if (!mbar_wait_warp(&pv_done[t], (sit - 1) & 1, abort, status)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < DH; c += 32) {
+              uint32_t ov[32];
+              tmem_ld32(o_tmem + c, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+              tmem_st16(o_tmem + c, *reinterpret_cast<const uint32_t(*)[16]>(&ov[0]));
+              tmem_st16(o_tmem + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&ov[16]));
+            }
+          }
+          float ls = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            if (some & (1u << c)) {
+              uint32_t v[32];
+              tmem_ld32(s_tmem + c * 32, v);
+              const uint32_t see = word(c);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float p0 = ex2(fmaf(__uint_as_float(v[2 * e]), sl2, -m_ref)), p1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), sl2, -m_ref));
+                if (!((see >> (2 * e)) & 1)) p0 = 0.f;
+                if (!((see >> (2 * e + 1)) & 1)) p1 = 0.f;
+                ls += p0 + p1;
+                const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
+                pk[e] = *(const uint32_t*)&hb;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0;
+            }
+            // (P of chunk c goes over scores of chunks that are done: columns 16 c .. 16 c + 15)
+            tmem_st16(s_tmem + c * 16, pk);
+            if (c & 1) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(c == 1 ? &p_half[t] : &p_full[t]);
+            }
+          }
+          l += ls;
+          continue;
+        }
+        const bool edge = !SPLIT && diag;  // this step's scores are masked
         auto seen = [&](int c) { return WN ? ((see[c >> 5] >> (c & 31)) & 1u) != 0 : c <= lim; };
         // pass 1: row maximum of the raw scores (four TMEM loads behind one wait; 3-input
         // max); only the diagonal tile needs the causal mask (a warp-uniform branch)
@@ -682,7 +764,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + c * 32, v[c]);
           tmem_ld_wait();
-          if (diag) {
+          if (edge) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -754,7 +836,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const float2 x2 = __ffma2_rn(make_float2(__uint_as_float(vb[c & 1][2 * e]), __uint_as_float(vb[c & 1][2 * e + 1])),
                                          sl2v, nmv);
             float p0 = ex2(x2.x), p1 = ex2(x2.y);
-            if (diag) {
+            if (edge) {
               if (!seen(c * 32 + 2 * e)) p0 = 0.f;
               if (!seen(c * 32 + 2 * e + 1)) p1 = 0.f;
             }
@@ -845,11 +927,11 @@ template <int DH, int MODE>
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                         int* status, int grid, cudaStream_t s) {
   constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES
-                                          : MODE == 2 ? (tca::MAX_RAGGED + 4) * 4 : 0);
-  cudaError_t e = MODE == 2 ? raise_max_smem(tca::attn_tc_kernel<DH, MODE>, sm)
+                                          : MODE >= 2 ? (tca::MAX_RAGGED + 4) * 4 : 0);
+  cudaError_t e = MODE >= 2 ? raise_max_smem(tca::attn_tc_kernel<DH, MODE>, sm)
                             : set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
   if (e != cudaSuccess) return e;
-  if (MODE == 2) return launch_dependent(tca::attn_tc_kernel<DH, MODE>, grid, tca::NTHREADS, sm, s, tq, tk, tv, a, status);
+  if (MODE >= 2) return launch_dependent(tca::attn_tc_kernel<DH, MODE>, grid, tca::NTHREADS, sm, s, tq, tk, tv, a, status);
   tca::attn_tc_kernel<DH, MODE><<<grid, tca::NTHREADS, sm, s>>>(tq, tk, tv, a, status);
   return cudaGetLastError();
 }
@@ -912,6 +994,11 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
     // (a window's items run side by side over a few windows of keys: one chunk of all streams)
     c.chunk = kv_bytes <= 0.5 * l2 || a.window ? NS : (want < 1 ? 1 : (want > NS ? NS : want));
   }
+  // Long windows: the masked steps apart, which slows those (serial chunks) and speeds the others.  1 x
+  // 32768, 32/8 heads, in turn: window 4096 2105 -> 2010 us, 1024 785 -> 775, 512 464 -> 496, 256 330 -> 390.
+  if (win && (a.window == 0 || a.window >= 1024))
+    return a.dh == 128 ? launch_attn<128, 3>(tq, tk, tv, c, status, grid, s)
+                       : launch_attn<64, 3>(tq, tk, tv, c, status, grid, s);
   if (win)
     return a.dh == 128 ? launch_attn<128, 2>(tq, tk, tv, c, status, grid, s)
                        : launch_attn<64, 2>(tq, tk, tv, c, status, grid, s);
