@@ -122,6 +122,25 @@ def test_append_of_special_values(mka):
 
 
 @pytest.mark.gpu
+def test_scales_that_jump(mka):
+    """Codes re-rounded to scales 2^1 .. 2^60 as large on append, and 2^1 .. 2^18 as small on eviction."""
+    c = mka.make_kv8_config(1, 64 * 16, 1, 1, 64, block=16, dtype="f32")
+    c2 = mka.make_kv8_config(1, 15 * 64, 1, 1, 64, block=16, dtype="f32")
+    g = gen(9)
+    cache, models = new_cache(mka, c), models_of(c)
+    for tb in range(64):  # 15 rows of codes of every size, then one row 2^tb times the block's scale
+        x = torch.randn(1, 15, 1, 64, generator=g) * torch.exp2(torch.randint(-9, 1, (1, 15, 1, 64), generator=g) * 1.0)
+        append(mka, c, cache, models, x, x.neg(), [16 * tb])
+        check_cache(mka, c, cache, models, [16 * tb + 15])
+        y = torch.randn(1, 1, 1, 64, generator=g) * 2.0 ** (tb if tb < 40 else tb - 40)
+        append(mka, c, cache, models, y, y, [16 * tb + 15])
+    check_cache(mka, c, cache, models, [64 * 16])
+    w = torch.ones(1, 1, 64 * 16)
+    w[0, 0, 15::16] = 0  # the large rows go
+    check_evict(mka, c, models, [64 * 16], w, 15 * 64, 0, 0, c2, evict(mka, c, cache, [64 * 16], w, 15 * 64, 0, 0, c2))
+
+
+@pytest.mark.gpu
 def test_append_past_the_end_and_before_the_start(mka):
     c = mka.make_kv8_config(3, 40, 1, 1, 64, block=16)
     cache, models = new_cache(mka, c), models_of(c)
