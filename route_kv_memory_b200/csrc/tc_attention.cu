@@ -165,8 +165,11 @@ __device__ __forceinline__ GroupPair window_pair(int w, const AttnArgs& a, const
 }
 // The item's tiles t = 0, 1: query tile qt[t] of head h[t] (len rows in use; a last odd tile's partner lies
 // behind them).  Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
-struct WWork {
-  int b, g, qt0, qt1, h0, h1, len, lo, nsk, n0, n1, s1;
+// The loader works it out and hands it to the other warps through two slots in shared memory: worked out
+// by each, its divisions cost every item some 3500 cycles of the softmax warps (1 x 32768, 32/8 heads,
+// window 1024: ITEMS_NOTE).
+struct __align__(16) WWork {
+  int b, g, qt0, qt1, h0, h1, len, lo, nsk, n0, n1, s1;  // b < 0: no more items
   __device__ __forceinline__ int key_tile(int j) const { return j == 0 ? lo : (j <= nsk ? j - 1 : lo + j - nsk); }
 };
 __device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, const int* first) {
@@ -231,6 +234,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* p_half = bars + 18;   // [2] keys 0-63 of P_t are in TMEM
   uint64_t* drain = bars + 20;
   uint32_t* tmem_slot = (uint32_t*)(bars + 21);
+  uint64_t* item_full = bars + 22;   // MODE 2, 3: [2] item slots
+  uint64_t* item_empty = bars + 24;  // [2]
+  WWork* items = (WWork*)(smem + 2 * C::Q_BYTES + 2 * C::KV_BYTES + 256);
   int* stok = (int*)(smem + 2 * C::Q_BYTES + 2 * C::KV_BYTES + 256);  // MODE 1: loader's tokens, [2][BQ]
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -250,6 +256,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&p_half[i], 4);
     }
     mbar_init(drain, 1);
+    if (WN) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&item_full[i], 1);
+        mbar_init(&item_empty[i], 9);  // the MMA warp and the softmax warps
+      }
+    }
     *abort = 0;
     fence_barrier_init();
   }
@@ -271,30 +283,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int G = a.Hq / a.Hkv;
   const int nbj = a.B * a.nblk;
   int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : WN ? a.B * a.Hkv * window_pairs(a.S, G) : a.B * a.Hq * npairs;
-  const int* first = nullptr;  // MODE 2, padded batches: see window_pair
-  if constexpr (WN) {
-    if (a.lens && a.B <= MAX_RAGGED) {
-      int* sfirst = (int*)(smem + 2 * C::Q_BYTES + 2 * C::KV_BYTES + 256);
-      if (warp == 0) {  // prefix sums of the sequences' items, 32 at a time
-        int sum = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-          const int b = b0 + lane, n = b < a.B ? window_pairs(min(max(a.lens[b], 0), a.S), G) * a.Hkv : 0;
-          int inc = n;
+  const int* first = nullptr;  // MODE 2, 3, padded batches (loader): see window_pair
+  if (WN && warp == 0 && a.lens && a.B <= MAX_RAGGED) {  // prefix sums of the sequences' items, 32 at a time
+    int* sfirst = (int*)(items + 2);
+    int sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane, n = b < a.B ? window_pairs(min(max(a.lens[b], 0), a.S), G) * a.Hkv : 0;
+      int inc = n;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-          }
-          if (b < a.B) sfirst[b] = sum + inc - n;
-          sum += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (lane == 0) sfirst[a.B] = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
       }
-      __syncthreads();
-      first = sfirst;
-      nwork = sfirst[a.B];
+      if (b < a.B) sfirst[b] = sum + inc - n;
+      sum += __shfl_sync(0xffffffffu, inc, 31);
     }
+    if (lane == 0) sfirst[a.B] = sum;
+    __syncwarp();
+    first = sfirst;
+    nwork = sum;
   }
+  // MODE 2, 3: the it-th item (whole warp); false when there is none, or the kernel unwinds
+  auto take_item = [&](int it, WWork& x) {
+    if (!mbar_wait_warp(&item_full[it & 1], (it >> 1) & 1, abort, status)) return false;
+    x = items[it & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[it & 1]);
+    return x.b >= 0;
+  };
   const int RPT = gathered_rows_per_token(G);  // MODE 1: tile rows per token (its G heads first)
   const int tpt = BQ / RPT;                    // MODE 1: tokens per query tile
   const long long q_rows_per_b = a.q_bstride / a.q_ld;
@@ -424,7 +440,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         WWork ww;
         if constexpr (WN) {
           ww = window_item(w, a, first);
-          if (ww.n1 == 0) continue;  // (every role skips the same items)
+          if (ww.n1 == 0) continue;
+          if (!mbar_wait(&item_empty[done & 1], ((done >> 1) & 1) ^ 1, abort, status)) break;
+          items[done & 1] = ww;
+          mbar_arrive(&item_full[done & 1]);
           it = {ww.b, ww.h0, 0};
         } else {
           it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
@@ -462,11 +481,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!ok) break;
       }
+      if (WN && mbar_wait(&item_empty[done & 1], ((done >> 1) & 1) ^ 1, abort, status)) {
+        items[done & 1].b = -1;
+        mbar_arrive(&item_full[done & 1]);
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp runs the role, converged; one elected lane issues)
-    int kvit = 0, pc[2] = {0, 0}, done = 0;
+    int kvit = 0, pc[2] = {0, 0};
     bool ok = true;
     WWork ww = {};
     // The K/V tile of step j (key tile kt of the current item) has landed in its stage; MODE 2 clears
@@ -512,16 +535,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int w0 = snake_item(0, gridDim.x, blockIdx.x, nwork);
       if (w0 >= 0) item_tiles(w0, nx0, nx1);
     }
-    for (int rr = 0; rr * (int)gridDim.x < nwork && ok; ++rr) {
-      const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
+    for (int rr = 0; (WN || rr * (int)gridDim.x < nwork) && ok; ++rr) {
+      const int w = WN ? 0 : snake_item(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       if constexpr (WN) {
-        ww = window_item(w, a, first);
-        if (ww.n1 == 0) continue;
+        if (!take_item(rr, ww)) break;
         nx0 = ww.n0;
         nx1 = ww.n1;
       }
-      const int wi = done++;  // items this CTA has started before this one
+      const int wi = rr;  // items this CTA has started before this one
       const int n0 = nx0, n1 = nx1;  // n0 <= n1, n1 >= 1
       const int s1 = WN ? ww.s1 : 0;  // tile 1's first step
       if (!mbar_wait_warp(&q_full[0], wi & 1, abort, status)) break;
@@ -613,17 +635,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // causal output rows start on 32-byte boundaries: one 32-byte store per 16 columns
     const bool o32 = !GA && ((uintptr_t)a.o & 31) == 0 && a.o_ld % 16 == 0 && a.o_bstride % 16 == 0;
     const uint64_t pol_out = policy_evict_first();  // output rows: written once, not read here
-    int sit = 0, done = 0;
-    for (int rr = 0; rr * (int)gridDim.x < nwork; ++rr) {
-      const int w = snake_item(rr, gridDim.x, blockIdx.x, nwork);
+    int sit = 0;
+    for (int rr = 0; WN || rr * (int)gridDim.x < nwork; ++rr) {
+      const int w = WN ? 0 : snake_item(rr, gridDim.x, blockIdx.x, nwork);
       if (w < 0) break;
       WWork ww;
       int j0 = 0;  // first step of this tile
       if constexpr (WN) {
-        ww = window_item(w, a, first);
-        if (ww.n1 == 0) continue;
+        if (!take_item(rr, ww)) break;
       }
-      const int wi = done++;
+      const int wi = rr;
       // This row: causal, position `row` of query head h of sequence b; MODE 1, the token of
       // entry e of the item's list (-1 for a padding row), query head h of KV group g.
       int b, h, row, nkv, slot = 0, key0 = 0;
@@ -927,7 +948,7 @@ template <int DH, int MODE>
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a,
                         int* status, int grid, cudaStream_t s) {
   constexpr int sm = tca::Cfg<DH>::SMEM + (MODE == 1 ? tca::Cfg<DH>::GATHER_BYTES
-                                          : MODE >= 2 ? (tca::MAX_RAGGED + 4) * 4 : 0);
+                                          : MODE >= 2 ? 2 * sizeof(tca::WWork) + (tca::MAX_RAGGED + 4) * 4 : 0);
   cudaError_t e = MODE >= 2 ? raise_max_smem(tca::attn_tc_kernel<DH, MODE>, sm)
                             : set_max_smem(tca::attn_tc_kernel<DH, MODE>, sm, s);
   if (e != cudaSuccess) return e;
