@@ -9,7 +9,6 @@ load, importing this package raises.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import Optional
 
@@ -18,10 +17,13 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmka.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python route_kv_memory_b200/_build.py` "
-                      "(or __graft_entry__.build()); this package has no CPU fallback")
+for _lib_file in (LIB_PATH, os.path.join(_PKG, "_binding.so")):
+    if not os.path.exists(_lib_file):
+        raise ImportError(f"{_lib_file} is missing: build it with `python route_kv_memory_b200/_build.py` "
+                          "(or __graft_entry__.build()); this package has no CPU fallback")
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _binding  # noqa: E402  (linked to the library just loaded; built with it)
 
 MKA_OK = 0
 MKA_ERR_INVALID_ARG = -1
@@ -265,60 +267,8 @@ def mka_decode_step(c: mka_config, packed, state, max_positions: int, x_new, out
 
 
 # ------------------------------------------------------------------ bounded-memory attention
-def _call_stream(tensors, stream, *caches):
-    """The stream pointer of a call on `tensors` (and 8-bit caches): they must live on the current device, and
-    a stream other than the current one is recorded on them."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor of the call must live on the current CUDA device ({dev})")
-    for x in caches:
-        if x.tensors[0].get_device() != dev:  # (its tensors share a device)
-            raise ValueError(f"the cache must live on the current CUDA device ({dev})")
-    current = torch._C._cuda_getCurrentRawStream(dev)  # (a Stream object per call would cost microseconds)
-    if stream is None:
-        return current
-    if stream.cuda_stream != current:
-        for x in caches:
-            tensors = (*tensors, *x.tensors)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    return stream.cuda_stream
-
-
-def _dense(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, *shape: int):
-    """Pointer of a contiguous tensor of that type and number of elements (None passes)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != math.prod(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} with {shape} elements, not {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _positions(t: Optional[torch.Tensor], name: str, B: int):
-    """Pointer of one int32 per sequence (None passes)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.int32 or t.numel() != B or not t.is_contiguous():
-        raise ValueError(f"{name} must be {B} contiguous int32, not {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _row_stride(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, S: int, heads: int, dh: int) -> int:
-    """Row stride of t [B, S, heads, dh] or [B, S, heads * dh] (see mka_attn_strides)."""
-    width, shape = heads * dh, t.shape
-    if t.dtype is not dtype or (shape != (B, S, heads, dh) and shape != (B, S, width)):
-        raise ValueError(f"{name} must be {dtype} [{B}, {S}, {heads}, {dh}] or [{B}, {S}, {width}], not {t.dtype} {tuple(shape)}")
-    if t.is_contiguous():
-        return width
-    st = t.stride()
-    ld = st[1] if S > 1 else (st[0] if B > 1 else width)
-    if st[-1] != 1 or (len(st) == 4 and heads > 1 and st[2] != dh) or (B > 1 and st[0] != S * ld):
-        raise ValueError(f"{name}: rows must be contiguous and evenly spaced over the whole batch, strides {st}")
-    return ld
-
-
+# (arguments are checked and passed on in csrc/binding.cpp; every tensor must live on the current device, and a
+# stream given here that is not the current one is recorded on them)
 def make_attn_config(batch: int, seq: int, n_q_heads: int, n_kv_heads: int, d_head: int, window: int = 0, sinks: int = 0,
                      attn_scale: Optional[float] = None) -> mka_attn_config:
     """Shape of a window attention call: window 0 sees every earlier position."""
@@ -331,20 +281,10 @@ def attention_lse(c: mka_attn_config, device="cuda") -> torch.Tensor:
     return torch.empty(c.batch, c.n_q_heads, (c.seq + 127) // 128 * 128, dtype=torch.float32, device=device)
 
 
-def _lse_ptr(c: mka_attn_config, lse):
-    return _dense(lse, "lse", torch.float32, c.batch, c.n_q_heads, (c.seq + 127) // 128 * 128)
-
-
 def mka_window_attention(c: mka_attn_config, q, k, v, lens, out, lse=None, stream=None) -> None:
     """q, out [B, S, Hq, dh] (or flat heads), k, v [B, S, Hkv, dh] bf16, row strides allowed; lens [B] int32
     or None; lse from attention_lse() or None."""
-    bf, B, S, H, G, d = torch.bfloat16, c.batch, c.seq, c.n_q_heads, c.n_kv_heads, c.d_head
-    s = _call_stream((q, k, v, lens, out, lse), stream)
-    st = mka_attn_strides(_row_stride(q, "q", bf, B, S, H, d), _row_stride(k, "k", bf, B, S, G, d),
-                          _row_stride(v, "v", bf, B, S, G, d), _row_stride(out, "out", bf, B, S, H, d), 0)
-    _check(_lib.mka_window_attention(c, st, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                     _positions(lens, "lens", B), out.data_ptr(), _lse_ptr(c, lse), s),
-           "mka_window_attention")
+    _check(_binding.window_attention(c, q, k, v, lens, out, lse, stream), "mka_window_attention")
 
 
 def mka_window_attention_backward_workspace_size(c: mka_attn_config) -> int:
@@ -353,16 +293,8 @@ def mka_window_attention_backward_workspace_size(c: mka_attn_config) -> int:
 
 def mka_window_attention_backward(c: mka_attn_config, q, k, v, out, lse, dout, lens, dq, dk, dv, ws, stream=None) -> None:
     """Gradients of sum(dout * out) after mka_window_attention(c, q, k, v, lens, out, lse): dq, dk, dv bf16, dense."""
-    bf, B, S, H, G, d = torch.bfloat16, c.batch, c.seq, c.n_q_heads, c.n_kv_heads, c.d_head
-    s = _call_stream((q, k, v, out, lse, dout, lens, dq, dk, dv, ws), stream)
-    st = mka_attn_strides(_row_stride(q, "q", bf, B, S, H, d), _row_stride(k, "k", bf, B, S, G, d),
-                          _row_stride(v, "v", bf, B, S, G, d), _row_stride(out, "out", bf, B, S, H, d),
-                          _row_stride(dout, "dout", bf, B, S, H, d))
-    _check(_lib.mka_window_attention_backward(
-        c, st, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _lse_ptr(c, lse), dout.data_ptr(),
-        _positions(lens, "lens", B), _dense(dq, "dq", bf, B, S, H * d), _dense(dk, "dk", bf, B, S, G * d),
-        _dense(dv, "dv", bf, B, S, G * d), ws.data_ptr(), ws.numel() * ws.element_size(), s),
-        "mka_window_attention_backward")
+    _check(_binding.window_attention_backward(c, q, k, v, out, lse, dout, lens, dq, dk, dv, ws, stream),
+           "mka_window_attention_backward")
 
 
 def make_kv8_config(batch: int, max_positions: int, n_q_heads: int, n_kv_heads: int, d_head: int, block: int = 64,
@@ -388,60 +320,18 @@ def kv8_cache(k, v, k_scale, v_scale) -> mka_kv8_cache:
         raise ValueError("the tensors of an 8-bit cache must live on one device")
     x = mka_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
     x.tensors = (k, v, k_scale, v_scale)
-    x.shapes = (*k.shape, *k_scale.shape)
     return x
-
-
-def _check_cache(c: mka_kv8_config, x: mka_kv8_cache) -> None:
-    B, H, L, blk = c.batch, c.n_kv_heads, c.max_positions, c.block
-    if x.shapes != (B, H, L, c.d_head, B, H, -(-L // blk) if blk > 0 else 0):
-        raise ValueError(f"the cache's codes and scales are {x.shapes[:4]}, {x.shapes[4:]}, not what the configuration says")
-
-
-def _kv_rows(c: mka_kv8_config, t: torch.Tensor, name: str):
-    """(rows, row stride, batch stride) of K/V rows [B, n, Hkv, dh] or [B, n, Hkv * dh]."""
-    want = torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32
-    if t.dtype is not want:
-        raise ValueError(f"{name} must be {want}, not {t.dtype}")
-    B, H, d, shape, st = c.batch, c.n_kv_heads, c.d_head, t.shape, t.stride()
-    n = shape[1] if len(shape) > 2 else -1
-    if shape == (B, n, H, d):
-        packed = st[3] == 1 and (H == 1 or st[2] == d)
-    elif shape == (B, n, H * d):
-        packed = st[2] == 1
-    else:
-        raise ValueError(f"{name} must be [{B}, n, {H}, {d}], not {tuple(shape)}")
-    if not packed:
-        raise ValueError(f"{name}: the elements of a row must be contiguous, strides {st}")
-    return n, (st[1] if n > 1 else H * d), (st[0] if B > 1 else 0)
-
-
-def _kv_pair(c: mka_kv8_config, k: torch.Tensor, v: torch.Tensor, names: str):
-    rows = _kv_rows(c, k, names[0])
-    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride():
-        raise ValueError(f"{names[0]} and {names[1]} must have the same type, shape and strides")
-    return rows
 
 
 def mka_kv8_append(c: mka_kv8_config, cache: mka_kv8_cache, k_new, v_new, pos, count=None, stream=None) -> None:
     """k_new, v_new [B, n, Hkv, dh] of the configuration's type (row and batch strides allowed, the same for both);
     pos, count [B] int32 on the device."""
-    s = _call_stream((k_new, v_new, pos, count), stream, cache)
-    _check_cache(c, cache)
-    rows = _kv_pair(c, k_new, v_new, ("k_new", "v_new"))
-    _check(_lib.mka_kv8_append(c, cache, k_new.data_ptr(), v_new.data_ptr(), rows[1], rows[2], rows[0],
-                               _positions(pos, "pos", c.batch), _positions(count, "count", c.batch), s),
-           "mka_kv8_append")
+    _check(_binding.kv8_append(c, cache, k_new, v_new, pos, count, stream), "mka_kv8_append")
 
 
 def mka_kv8_read(c: mka_kv8_config, cache: mka_kv8_cache, first, rows, k_out, v_out, stream=None) -> None:
     """Values of positions first[b] .. first[b] + rows[b] - 1 to k_out, v_out [B, n, Hkv, dh] (strides allowed)."""
-    s = _call_stream((first, rows, k_out, v_out), stream, cache)
-    _check_cache(c, cache)
-    at = _kv_pair(c, k_out, v_out, ("k_out", "v_out"))
-    _check(_lib.mka_kv8_read(c, cache, _positions(first, "first", c.batch),
-                             _positions(rows, "rows", c.batch), at[0], k_out.data_ptr(), v_out.data_ptr(), at[1],
-                             at[2], s), "mka_kv8_read")
+    _check(_binding.kv8_read(c, cache, first, rows, k_out, v_out, stream), "mka_kv8_read")
 
 
 def mka_kv8_attention_workspace_size(c: mka_kv8_config, n: int = 1, with_weights: bool = False) -> int:
@@ -451,15 +341,7 @@ def mka_kv8_attention_workspace_size(c: mka_kv8_config, n: int = 1, with_weights
 def mka_kv8_attention(c: mka_kv8_config, cache: mka_kv8_cache, q, lens, out, weights, ws, stream=None) -> None:
     """Attention of the last n positions: q, out [B, n, Hq, dh] (or flat heads), dense; lens [B] int32 on the device;
     weights [B, Hkv, max_positions] float32 or None."""
-    s = _call_stream((q, lens, out, weights, ws), stream, cache)
-    _check_cache(c, cache)
-    dt = torch.bfloat16 if c.dtype == MKA_BF16 else torch.float32
-    n = q.shape[1] if q.dim() >= 2 else 0
-    _check(_lib.mka_kv8_attention(
-        c, cache, _dense(q, "q", dt, c.batch, n, c.n_q_heads * c.d_head), n, _positions(lens, "lens", c.batch),
-        _dense(out, "out", dt, c.batch, n, c.n_q_heads * c.d_head),
-        _dense(weights, "weights", torch.float32, c.batch, c.n_kv_heads, c.max_positions), ws.data_ptr(),
-        ws.numel() * ws.element_size(), s), "mka_kv8_attention")
+    _check(_binding.kv8_attention(c, cache, q, lens, out, weights, ws, stream), "mka_kv8_attention")
 
 
 def mka_kv8_evict_workspace_size(c: mka_kv8_config, keep: int) -> int:
@@ -469,15 +351,8 @@ def mka_kv8_evict_workspace_size(c: mka_kv8_config, keep: int) -> int:
 def mka_kv8_evict(c: mka_kv8_config, cache: mka_kv8_cache, lens, weights, keep: int, first: int, recent: int,
                   dst_c: mka_kv8_config, dst: mka_kv8_cache, dst_lens, dst_weights, kept, ws, stream=None) -> None:
     """Keeps `keep` positions of every sequence and KV head (the first, the last, the heaviest) in another cache."""
-    s = _call_stream((lens, weights, dst_lens, dst_weights, kept, ws), stream, cache, dst)
-    _check_cache(c, cache)
-    _check_cache(dst_c, dst)
-    B, H = c.batch, c.n_kv_heads
-    _check(_lib.mka_kv8_evict(
-        c, cache, _positions(lens, "lens", B), _dense(weights, "weights", torch.float32, B, H, c.max_positions),
-        keep, first, recent, dst_c, dst, _positions(dst_lens, "dst_lens", B),
-        _dense(dst_weights, "dst_weights", torch.float32, B, H, dst_c.max_positions),
-        _dense(kept, "kept", torch.int32, B, H, keep), ws.data_ptr(), ws.numel() * ws.element_size(), s), "mka_kv8_evict")
+    _check(_binding.kv8_evict(c, cache, lens, weights, keep, first, recent, dst_c, dst, dst_lens, dst_weights, kept, ws,
+                              stream), "mka_kv8_evict")
 
 
 def mka_status() -> int:

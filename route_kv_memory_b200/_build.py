@@ -1,4 +1,4 @@
-"""Build libmka.so (sm_100a) in-tree with nvcc.
+"""Build libmka.so (sm_100a) in-tree with nvcc, and the Python binding of its bounded-memory operators.
 
     python route_kv_memory_b200/_build.py          # incremental
     python route_kv_memory_b200/_build.py --force  # rebuild everything
@@ -12,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmka.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["api.cu", "gemm.cu", "memory.cu", "attention.cu", "decode.cu", "noalloc.cu", "api_bounded.cu", "kv8.cu", "tc_gemm.cu", "tc_attention.cu", "block_sparse.cu", "tc_attention_bwd.cu", "backward.cu", "selftest.cu"]
 HEADERS = ["common.cuh", "kernels.h", "sm100.cuh"]
 
@@ -68,7 +70,30 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_binding(force)
     return LIB
+
+
+def _build_binding(force: bool) -> None:
+    """_binding.so: argument marshalling against torch's headers, linked to libmka.so beside it."""
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "mka.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-isystem" + p for p in inc), src, "-o", tmp,
+           "-L" + PKG, "-l:libmka.so", "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

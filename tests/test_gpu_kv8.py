@@ -528,11 +528,38 @@ def test_binding_refuses_shapes(mka):
         with pytest.raises(ValueError):
             mka.kv8_cache(*bad)
     x = mka.kv8_cache(t, t.clone(), s, s.clone())
-    with pytest.raises(ValueError):
-        mka._check_cache(cfg(mka, max_positions=301), x)
-    with pytest.raises(ValueError):
-        mka._check_cache(cfg(mka, block=32), x)
+    good, pos = torch.zeros(2, 3, 2, 64).bfloat16(), torch.zeros(2, dtype=torch.int32)
+    q, ws = torch.zeros(2, 1, 4, 64).bfloat16(), torch.zeros(16, dtype=torch.uint8)
+    for c in (cfg(mka, max_positions=301), cfg(mka, block=32), cfg(mka, batch=1)):
+        with pytest.raises(ValueError, match="cache's"):
+            mka.mka_kv8_append(c, x, good, good, pos)
     for bad in (torch.zeros(2, 3, 2, 64), torch.zeros(1, 3, 2, 64).bfloat16(), torch.zeros(2, 3, 2, 128).bfloat16()[..., ::2],
-                torch.zeros(2, 3, 2, 128).bfloat16()[..., :64], torch.zeros(2, 128).bfloat16()):
-        with pytest.raises(ValueError):
-            mka._kv_rows(cfg(mka), bad, "k_new")
+                torch.zeros(2, 3, 2, 128).bfloat16()[..., :64], torch.zeros(2, 128).bfloat16(), good.transpose(0, 1), None):
+        with pytest.raises(ValueError, match="k_new"):
+            mka.mka_kv8_append(cfg(mka), x, bad, bad, pos)
+        with pytest.raises(ValueError, match="k_out"):
+            mka.mka_kv8_read(cfg(mka), x, None, pos, bad, bad)
+    with pytest.raises(ValueError, match="same"):
+        mka.mka_kv8_append(cfg(mka), x, good, good[:, :2], pos)
+    for p in (pos[:1], pos.long(), torch.zeros(4, dtype=torch.int32)[::2], 3):
+        with pytest.raises(ValueError, match="pos"):
+            mka.mka_kv8_append(cfg(mka), x, good, good, p)
+        with pytest.raises(ValueError, match="lens"):
+            mka.mka_kv8_attention(cfg(mka), x, q, p, q, None, ws)
+    for p in (q.float(), q[:1], q[..., ::2], q[0]):
+        with pytest.raises(ValueError, match="must be"):
+            mka.mka_kv8_attention(cfg(mka), x, p, pos, q, None, ws)
+    with pytest.raises(ValueError, match="weights"):
+        mka.mka_kv8_attention(cfg(mka), x, q, pos, q, torch.zeros(2, 2, 299), ws)
+    with pytest.raises(ValueError, match="structure"):
+        mka.mka_kv8_append(mka.make_attn_config(1, 1, 1, 1, 64), x, good, good, pos)
+    with pytest.raises(ValueError, match="kv8_cache|tensor"):
+        y = fake(mka)
+        y.tensors = (1, 2, 3, 4)
+        mka.mka_kv8_append(cfg(mka), y, good, good, pos)
+    with pytest.raises(AttributeError):
+        mka.mka_kv8_append(cfg(mka), fake(mka), good, good, pos)
+    with pytest.raises(TypeError):
+        mka.mka_kv8_append(None, x, good, good, pos)
+    with pytest.raises(ValueError, match="range|kept"):
+        mka.mka_kv8_evict(cfg(mka), x, pos, torch.zeros(2, 2, 300), 1 << 40, 0, 0, cfg(mka), x, pos, None, pos, ws)

@@ -253,8 +253,10 @@ def test_binding_refuses_shapes_types_and_devices(mka):
         mka.mka_window_attention(c, q[:, :299], k, k, None, out)
     with pytest.raises(ValueError):
         mka.mka_window_attention(c, q.float(), k, k, None, out)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="current CUDA device"):
         mka.mka_window_attention(c, q.cpu(), k, k, None, out)
+    with pytest.raises(ValueError, match="lens"):
+        mka.mka_window_attention(c, q, k, k, [300, 300], out)
     with pytest.raises(ValueError):
         mka.mka_window_attention(c, q, k, k, torch.zeros(3, dtype=torch.int32, device="cuda"), out)
     with pytest.raises(ValueError):
