@@ -132,37 +132,6 @@ __device__ __forceinline__ int entry_token(int v, int S, int* slot) {
 // list of key tiles, so that both halves of the ping-pong have a tile in every step (two query tiles of one
 // head, as in MODE 0, leave each half idle for a step of every window; 1 x 32768, 32/8 heads, window 1024: 924 -> 840 us).
 __host__ __device__ __forceinline__ int window_pairs(int rows, int G) { return ((rows + BQ - 1) / BQ * G + 1) / 2; }
-// Item w as its sequence, group and P.  Padded batches: the items of rows in use only, sequence by
-// sequence, longest first, with first[b] the items in front of sequence b's (built per CTA from lens; the
-// static snake would otherwise give some CTAs mostly items behind the sequences' ends: 2 x 4096 with
-// 1006 rows in use in the second, 28/4 heads, window 1024: 150 -> 95 us).
-constexpr int MAX_RAGGED = 512;  // sequences; more: every item is enumerated and the empty ones skipped
-struct GroupPair {
-  int b, g, P;
-};
-__device__ __forceinline__ GroupPair window_pair(int w, const AttnArgs& a, const int* first) {
-  GroupPair r;
-  if (first) {
-    int lo = 0, hi = a.B;  // first[lo] <= w < first[hi]
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (first[m] <= w) lo = m;
-      else hi = m;
-    }
-    const int back = first[lo + 1] - 1 - w;
-    r.b = lo;
-    r.P = back / a.Hkv;
-    r.g = back % a.Hkv;
-  } else {  // as work_item: chunks of streams
-    const int np = window_pairs(a.S, a.Hq / a.Hkv), NS = a.B * a.Hkv;
-    const int k = w / (a.chunk * np), cs = min(a.chunk, NS - k * a.chunk), rem = w - k * a.chunk * np;
-    const int st = k * a.chunk + rem % cs;
-    r.P = np - 1 - rem / cs;
-    r.b = st / a.Hkv;
-    r.g = st % a.Hkv;
-  }
-  return r;
-}
 // The item's tiles t = 0, 1: query tile qt[t] of head h[t] (len rows in use; a last odd tile's partner lies
 // behind them).  Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
 // The loader works it out and hands it to the other warps through two slots in shared memory: worked out
@@ -172,19 +141,45 @@ struct __align__(16) WWork {
   int b, g, qt0, qt1, h0, h1, len, lo, nsk, n0, n1, s1;  // b < 0: no more items
   __device__ __forceinline__ int key_tile(int j) const { return j == 0 ? lo : (j <= nsk ? j - 1 : lo + j - nsk); }
 };
-__device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, const int* first) {
-  const GroupPair it = window_pair(w, a, first);
-  const int G = a.Hq / a.Hkv;
+// Item w's sequence, group and tiles (the steps left open).  Padded batches: the items of rows in use only,
+// sequence by sequence, longest first, with first[b] the items in front of sequence b's (built per CTA from
+// lens; the static snake would otherwise give some CTAs mostly items behind the sequences' ends: 2 x 4096
+// with 1006 rows in use in the second, 28/4 heads, window 1024: 150 -> 95 us).
+constexpr int MAX_RAGGED = 512;  // sequences; more: every item is enumerated and the empty ones skipped
+__device__ __forceinline__ WWork window_pair(int w, const AttnArgs& a, const int* first) {
   WWork r;
-  r.b = it.b;
-  r.g = it.g;
-  r.qt0 = 2 * it.P / G;
-  r.qt1 = (2 * it.P + 1) / G;
-  r.h0 = it.g * G + 2 * it.P % G;
-  r.h1 = it.g * G + (2 * it.P + 1) % G;
-  r.len = a.lens ? min(max(a.lens[it.b], 0), a.S) : a.S;
+  const int G = a.Hq / a.Hkv;
+  int P;
+  if (first) {
+    int lo = 0, hi = a.B;  // first[lo] <= w < first[hi]
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (first[m] <= w) lo = m;
+      else hi = m;
+    }
+    const int back = first[lo + 1] - 1 - w;
+    r.b = lo;
+    P = back / a.Hkv;
+    r.g = back % a.Hkv;
+  } else {  // as work_item: chunks of streams
+    const int np = window_pairs(a.S, G), NS = a.B * a.Hkv;
+    const int k = w / (a.chunk * np), cs = min(a.chunk, NS - k * a.chunk), rem = w - k * a.chunk * np;
+    const int st = k * a.chunk + rem % cs;
+    P = np - 1 - rem / cs;
+    r.b = st / a.Hkv;
+    r.g = st % a.Hkv;
+  }
+  r.qt0 = 2 * P / G;
+  r.qt1 = (2 * P + 1) / G;
+  r.h0 = r.g * G + 2 * P % G;
+  r.h1 = r.g * G + (2 * P + 1) % G;
+  return r;
+}
+// The rest of an item: its rows in use and its key tiles.
+__device__ __forceinline__ void window_steps(WWork& r, const AttnArgs& a) {
+  r.len = a.lens ? min(max(a.lens[r.b], 0), a.S) : a.S;
   r.n0 = r.n1 = r.s1 = r.lo = r.nsk = 0;
-  if (r.qt0 * BQ >= r.len) return r;
+  if (r.qt0 * BQ >= r.len) return;
   const int last = (r.len - 1) / BKV;
   const int lo0 = a.window ? max(0, r.qt0 * BQ - a.window + 1) / BKV : 0;
   const int lo1 = a.window ? max(0, r.qt1 * BQ - a.window + 1) / BKV : 0;
@@ -194,7 +189,6 @@ __device__ __forceinline__ WWork window_item(int w, const AttnArgs& a, const int
   r.n0 = 1 + r.nsk + r.qt0 - lo0;
   r.n1 = 1 + r.nsk + hi1 - lo0;
   r.s1 = lo1 > lo0 && lo0 * BKV >= a.sinks && hi1 > lo0 ? 1 : 0;
-  return r;
 }
 
 // Bits [0, n) of a 32-bit word, n clamped to [0, 32].
@@ -270,10 +264,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  if constexpr (WN) {
-    wait_previous_kernel();
-    allow_next_kernel();
-  }
+  // MODE 2, 3: what follows up to the first item runs under the end of the kernel in front; the loader waits for
+  // that before it touches memory, and every other access follows from its copies (the first item worked out
+  // in front of the wait: 1 x 255, 4/2 heads, 10.8 -> 9.75 us)
+  if constexpr (WN)
+    if (threadIdx.x != 0) allow_next_kernel();  // (thread 0, the loader, behind its wait)
   // TMEM column of O_t and of S_t / P_t
 #define O_COL(t) (128u * (uint32_t)(t))
 #define S_COL(t) (256u + 128u * (uint32_t)(t))
@@ -284,7 +279,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int nbj = a.B * a.nblk;
   int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : WN ? a.B * a.Hkv * window_pairs(a.S, G) : a.B * a.Hq * npairs;
   const int* first = nullptr;  // MODE 2, 3, padded batches (loader): see window_pair
-  if (WN && warp == 0 && a.lens && a.B <= MAX_RAGGED) {  // prefix sums of the sequences' items, 32 at a time
+  if (WN && threadIdx.x == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  // prefix sums of the sequences' items, 32 at a time (not where every item has a CTA of its own)
+  if (WN && warp == 0 && a.lens && a.B <= MAX_RAGGED && nwork > (int)gridDim.x) {
+    wait_previous_kernel();
     int* sfirst = (int*)(items + 2);
     int sum = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -313,8 +315,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   };
   const int RPT = gathered_rows_per_token(G);  // MODE 1: tile rows per token (its G heads first)
   const int tpt = BQ / RPT;                    // MODE 1: tokens per query tile
-  const long long q_rows_per_b = a.q_bstride / a.q_ld;
-  const long long kv_rows_per_b = a.kv_bstride / a.kv_ld;
+  const long long q_rows_per_b = WN ? a.S : a.q_bstride / a.q_ld;  // (MODE 2, 3: evenly spaced rows)
+  const long long kv_rows_per_b = WN ? a.S : a.kv_bstride / a.kv_ld;
   const int mt = GA ? a.blk / BKV : 1;  // MODE 1: key tiles per L3 block
   // Key tiles of the two query tiles of an item (n0 <= n1).  Causal: tile qt runs tiles 0..qt.
   // MODE 1: local tile t holds list tile 2p + 1 - t, so tile 1 always exists and tile 0 may be
@@ -426,9 +428,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (w >= 0) lookup(w);
       }
     } else if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
+      if constexpr (!WN) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
       // L2: a query tile is read by this item only, while the K/V of the chunk's streams are read
       // by every item of the chunk: the Q tiles (and the O rows) must not age the K/V out of L2
       const uint64_t pol_once = policy_evict_first(), pol_kv = policy_evict_last();
@@ -439,11 +443,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Work it;
         WWork ww;
         if constexpr (WN) {
-          ww = window_item(w, a, first);
+          ww = window_pair(w, a, first);
+          if (rr == 0 && a.lens) wait_previous_kernel();
+          window_steps(ww, a);
           if (ww.n1 == 0) continue;
           if (!mbar_wait(&item_empty[done & 1], ((done >> 1) & 1) ^ 1, abort, status)) break;
           items[done & 1] = ww;
           mbar_arrive(&item_full[done & 1]);
+          if (done == 0) {
+            wait_previous_kernel();
+            allow_next_kernel();
+          }
           it = {ww.b, ww.h0, 0};
         } else {
           it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
@@ -480,6 +490,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         if (!ok) break;
+      }
+      if (WN && done == 0) {  // (a CTA without items must not end in front of it either)
+        wait_previous_kernel();
+        allow_next_kernel();
       }
       if (WN && mbar_wait(&item_empty[done & 1], ((done >> 1) & 1) ^ 1, abort, status)) {
         items[done & 1].b = -1;

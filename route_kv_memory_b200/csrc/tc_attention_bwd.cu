@@ -125,13 +125,14 @@ __device__ __forceinline__ void init_slots(const ItemSlots& s) {
   }
 }
 // Loader thread: passes on the next item that is not `dead` as the rr-th (-1: no more).  Returns it, or -2
-// when the kernel unwinds.  order (nullable): the items in the order to give them.
+// when the kernel unwinds.  order (nullable): the items in the order to give them; with it, CTAs start
+// together and the first item of each is the one of its number, known without the counter.
 template <typename F>
 __device__ __forceinline__ int give_item(const ItemSlots& s, int rr, int* counter, int nwork, F dead,
                                          const int* order, volatile int* abort, int* status) {
   int w;
   do {
-    w = atomicAdd(counter, 1);
+    w = !order ? atomicAdd(counter, 1) : rr == 0 ? blockIdx.x : gridDim.x + atomicAdd(counter, 1);
     w = w < nwork ? w : -1;
   } while (w >= 0 && dead(w));
   if (order && w >= 0) w = order[w];
@@ -618,6 +619,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   if constexpr (WN) {
+    if (threadIdx.x == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmdO);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
     wait_previous_kernel();
     allow_next_kernel();
   }
