@@ -146,6 +146,7 @@ struct AttnArgs {
   bool windowed = false;
   int window = 0, sinks = 0;
   const int* lens = nullptr;
+  bool single = false;  // windowed: items of one query tile (set by attention_prefill_tc)
   long long v_bstride = 0; int v_ld = 0;  // V's own strides (0: kv_bstride, kv_ld)
   // Block-gathered attention (set g_pairoff to select it; bf16, tcgen05 only).  The rows of a
   // work item are (token, query head) pairs that all attend to the keys of one L3 block j of

@@ -132,6 +132,9 @@ __device__ __forceinline__ int entry_token(int v, int S, int* slot) {
 // list of key tiles, so that both halves of the ping-pong have a tile in every step (two query tiles of one
 // head, as in MODE 0, leave each half idle for a step of every window; 1 x 32768, 32/8 heads, window 1024: 924 -> 840 us).
 __host__ __device__ __forceinline__ int window_pairs(int rows, int G) { return ((rows + BQ - 1) / BQ * G + 1) / 2; }
+// Few query tiles (a.single): items of one tile, run as tile 1 beside an empty tile 0, so that twice as many SMs
+// take part and no tile waits for its partner's exponentials (1 x 255, 4/2 heads of 64: 9.3 -> 8.2 us;
+// 1 x 2304, 8/2 heads of 128, window 512: 18.8 -> 17.3 us).
 // The item's tiles t = 0, 1: query tile qt[t] of head h[t] (len rows in use; a last odd tile's partner lies
 // behind them).  Tile 0 runs steps [0, n0), tile 1 steps [s1, n1) of the key-tile list; n1 == 0: no row in use.
 // The loader works it out and hands it to the other warps through two slots in shared memory: worked out
@@ -162,17 +165,18 @@ __device__ __forceinline__ WWork window_pair(int w, const AttnArgs& a, const int
     P = back / a.Hkv;
     r.g = back % a.Hkv;
   } else {  // as work_item: chunks of streams
-    const int np = window_pairs(a.S, G), NS = a.B * a.Hkv;
+    const int np = a.single ? (a.S + BQ - 1) / BQ * G : window_pairs(a.S, G), NS = a.B * a.Hkv;
     const int k = w / (a.chunk * np), cs = min(a.chunk, NS - k * a.chunk), rem = w - k * a.chunk * np;
     const int st = k * a.chunk + rem % cs;
     P = np - 1 - rem / cs;
     r.b = st / a.Hkv;
     r.g = st % a.Hkv;
   }
-  r.qt0 = 2 * P / G;
-  r.qt1 = (2 * P + 1) / G;
-  r.h0 = r.g * G + 2 * P % G;
-  r.h1 = r.g * G + (2 * P + 1) % G;
+  const int f0 = a.single ? P : 2 * P, f1 = a.single ? P : 2 * P + 1;
+  r.qt0 = f0 / G;
+  r.qt1 = f1 / G;
+  r.h0 = r.g * G + f0 % G;
+  r.h1 = r.g * G + f1 % G;
   return r;
 }
 // The rest of an item: its rows in use and its key tiles.
@@ -186,7 +190,7 @@ __device__ __forceinline__ void window_steps(WWork& r, const AttnArgs& a) {
   const int hi1 = min(r.qt1, last);
   r.lo = lo0;
   r.nsk = min((a.sinks + BKV - 1) / BKV, lo0);
-  r.n0 = 1 + r.nsk + r.qt0 - lo0;
+  r.n0 = a.single ? 0 : 1 + r.nsk + r.qt0 - lo0;
   r.n1 = 1 + r.nsk + hi1 - lo0;
   r.s1 = lo1 > lo0 && lo0 * BKV >= a.sinks && hi1 > lo0 ? 1 : 0;
 }
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int npairs = (nqt + 1) / 2;
   const int G = a.Hq / a.Hkv;
   const int nbj = a.B * a.nblk;
-  int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : WN ? a.B * a.Hkv * window_pairs(a.S, G) : a.B * a.Hq * npairs;
+  int nwork = GA ? a.Hkv * a.g_pairoff[nbj] : WN ? a.B * (a.single ? a.Hq * nqt : a.Hkv * window_pairs(a.S, G)) : a.B * a.Hq * npairs;
   const int* first = nullptr;  // MODE 2, 3, padded batches (loader): see window_pair
   if (WN && threadIdx.x == 0) {
     tma_prefetch_desc(&tmQ);
@@ -465,6 +469,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!mbar_wait(&q_empty[t], (wi & 1) ^ 1, abort, status)) {
             qok = false;
             break;
+          }
+          if (WN && t == 0 && ww.n0 == 0) {
+            mbar_arrive(&q_full[0]);
+            continue;
           }
           mbar_expect_tx(&q_full[t], C::Q_BYTES);
           const int qy = (int)(it.b * q_rows_per_b) + (WN ? (t ? ww.qt1 : ww.qt0) : 2 * it.pair + t) * BQ;
@@ -908,7 +916,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         orow = (bf16*)a.part_o + ps * (size_t)(a.Hq * DH) + (size_t)h * DH;
         if (store) a.part_lse[ps * a.Hq + h] = m_ref + __log2f(l);
       } else {
-        store = row < (WN ? ww.len : a.S);
+        store = row < (WN ? ww.len : a.S) && (!WN || nkv > 0);
         orow = (bf16*)a.o + (size_t)b * a.o_bstride + (size_t)row * a.o_ld + (size_t)h * DH;
         if (a.lse && store) a.lse[((size_t)b * a.Hq + h) * a.lse_ld + row] = m_ref + __log2f(l);
       }
@@ -1011,7 +1019,9 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
     return cudaErrorInvalidValue;
   // MODE 1: the item count is on the device (block_lists); idle CTAs leave at once
   const int nqt = (a.S + tca::BQ - 1) / tca::BQ;
-  const int nwork = win ? a.B * a.Hkv * tca::window_pairs(a.S, a.Hq / a.Hkv) : a.B * a.Hq * ((nqt + 1) / 2);
+  const bool single = win && (long long)a.B * a.Hq * nqt <= sms;  // a CTA for every query tile
+  const int nwork = single ? a.B * a.Hq * nqt
+                    : win  ? a.B * a.Hkv * tca::window_pairs(a.S, a.Hq / a.Hkv) : a.B * a.Hq * ((nqt + 1) / 2);
   const int grid = ga ? sms : (nwork < sms ? nwork : sms);
   // causal mode: streams per chunk of the work order.  When the K/V of all streams fits in half of
   // L2, one chunk of all streams; otherwise the fewest streams for which one round of `grid` items
@@ -1020,6 +1030,7 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
   // from DRAM, where a single chunk read 174 GB; at 2 x 32768 (134 MB of K/V) chunks of 2 streams
   // take 14.08 ms against 14.45 ms for a single chunk.
   AttnArgs c = a;
+  c.single = single;
   if (!ga) {
     const int G = a.Hq / a.Hkv, NS = a.B * a.Hkv, npairs = (nqt + 1) / 2;
     int l2 = 0;
