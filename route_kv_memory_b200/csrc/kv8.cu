@@ -989,13 +989,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // The kept positions.  A cluster of CTAs per (sequence, KV head); every lane owns KPT consecutive
 // positions (a warp 32 KPT, a CTA 1024 KPT, rounds of them where the cluster's share is longer than that).
 // Three passes of 11, 11 and 10 bits find the key of the last kept token among the middle ones
-// [first, len - recent): each counts the digits of the keys that match the digits found so far, and the
-// CTAs add each other's counts through distributed shared memory.  Then everyone counts what it keeps --
+// [first, len - recent): each counts the digits of the keys that match the digits found so far, and a warp of
+// every CTA adds the cluster's counts through distributed shared memory, first those of blocks of 64 digits,
+// then those of the digits in the block that it needs (all 2048 of them, added in slices by the CTAs and
+// handed back: 2.7 us more).  Then everyone counts what it keeps --
 // forced tokens, keys above the found one, and of those equal to it the first `need` in position order --
 // and after a prefix sum over lanes, warps and CTAs writes it in order.  Keys are loaded coalesced and
 // turned to their owners through shared memory; a lane's matches are bits of one word, so that a token
 // costs a few instructions a pass.  Bound by the chain of passes and cluster barriers: 8 heads of 131072
-// positions 15 us (one CTA per head, four passes of atomics: 390 us).
+// positions about 12 us (one CTA per head, four passes of atomics: 390 us).
 constexpr int SEL_THREADS = 1024, SEL_WARPS = SEL_THREADS / 32, SEL_BINS = 2048, SEL_CLUSTER = 8;
 constexpr int KPT = 16;                     // positions per lane and round
 constexpr int SEL_ROUND = SEL_THREADS * KPT;
@@ -1009,9 +1011,11 @@ __device__ __forceinline__ int2 load_remote2(const int* p, uint32_t rank) {
                : "=r"(v.x), "=r"(v.y) : "r"(sm100::smem_u32(p)), "r"(rank) : "memory");
   return v;
 }
-__device__ __forceinline__ void store_remote2(int* p, uint32_t rank, int2 v) {
-  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tst.shared::cluster.v2.b32 [r], {%2, %3};\n\t}"
-               :: "r"(sm100::smem_u32(p)), "r"(rank), "r"(v.x), "r"(v.y) : "memory");
+__device__ __forceinline__ int load_remote(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.b32 %0, [r];\n\t}"
+               : "=r"(v) : "r"(sm100::smem_u32(p)), "r"(rank) : "memory");
+  return v;
 }
 __device__ __forceinline__ int warp_excl(int v, int lane) {  // exclusive prefix sum over the lanes
   int x = v;
@@ -1033,7 +1037,10 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weights, int Lmax, int Hkv, int CL, const int* lens,
                                                              int keep, int first, int recent, int* kept, int* lens2) {
   extern __shared__ uint32_t skeys[];
-  __shared__ __align__(8) int hist[SEL_BINS], all[SEL_BINS];  // this CTA's counts, the cluster's
+  // this CTA's counts of digits and of blocks of 64 digits; a pass takes the one buffer while others may still
+  // read the one of the pass before
+  __shared__ __align__(8) int counts[2][SEL_BINS];
+  __shared__ int blocks[2][SEL_WARPS];
   __shared__ __align__(8) int sTot[2];
   __shared__ int sWarp[2][SEL_WARPS], sPick[3];
   const int hd = blockIdx.x / CL, rank = blockIdx.x % CL, b = hd / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1071,7 +1078,9 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
     __syncwarp();
   };
   const bool once = rounds <= 1;  // the keys stay in shared memory from pass to pass
+  for (int i = threadIdx.x; i < 2 * SEL_BINS; i += SEL_THREADS) counts[0][i] = 0;
   if (once) load(0);
+  __syncthreads();
   int need = keep - first - recent;  // of the middle tokens; fewer than there are
   const bool none = need == 0;
   int low = 0;
@@ -1079,8 +1088,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
   for (int pass = 0; pass < 3 && !none; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     const uint32_t mask = (1u << bits) - 1;
-    for (int i = threadIdx.x; i < SEL_BINS; i += SEL_THREADS) hist[i] = 0;
-    __syncthreads();
+    int *hist = counts[pass & 1], *block = blocks[pass & 1];
     for (int q = 0; q < rounds; ++q) {
       const int p = cb + q * SEL_ROUND + (warp * 32 + lane) * KPT;
       if (!once) load(q);
@@ -1099,37 +1107,40 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
         for (uint32_t m = match; m; m &= m - 1) atomicAdd(&hist[(own[__ffs(m) - 1] >> shift) & mask], 1);
       }
     }
-    if (CL > 1) {
-      // every CTA adds up the counts of its slices of 256 bins, 8 lanes (a CTA's counts each) per pair of
-      // bins, and gives every CTA the sum
-      sm100::cluster_sync();
-      const int r = threadIdx.x % SEL_CLUSTER;
-      for (int sl = rank; sl < SEL_BINS / 256; sl += CL) {
-        int* bin = &hist[sl * 256 + threadIdx.x / SEL_CLUSTER * 2];
-        int2 c = r < CL ? load_remote2(bin, r) : make_int2(0, 0);
-#pragma unroll
-        for (int o = 1; o < SEL_CLUSTER; o <<= 1) {
-          c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
-          c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
-        }
-        if (r < CL) store_remote2(all + (bin - hist), r, c);
-      }
-      sm100::cluster_sync();  // (the next pass writes `all` only behind its own first barrier)
-    } else {
-      __syncthreads();
-    }
-    // bins from the largest down, two per thread: d and d - 1
-    const int d = SEL_BINS - 1 - 2 * threadIdx.x;
-    const int2 c = *(const int2*)&(CL > 1 ? all : hist)[d - 1];
-    int before = warp_excl(c.x + c.y, lane);
-    if (lane == 31) sWarp[0][warp] = before + c.x + c.y;
     __syncthreads();
-    before += __shfl_sync(0xffffffffu, warp_excl(sWarp[0][lane], lane), warp);
-    if (before < need && need <= before + c.x + c.y) {  // one thread
-      const bool second = need > before + c.y;
-      sPick[0] = second ? d - 1 : d;
-      sPick[1] = need - before - (second ? c.y : 0);
-      sPick[2] = second ? c.x : c.y;
+    {  // the blocks' counts, a warp each
+      const int2 c = *(const int2*)(hist + 2 * threadIdx.x);
+      const int n = __reduce_add_sync(0xffffffffu, c.x + c.y);
+      if (lane == 0) block[warp] = n;
+    }
+    sm100::cluster_sync();
+    if (warp == 0) {  // from the largest digit down: the block where the sum over the cluster reaches need, then its digit
+      int n[SEL_CLUSTER], sum = 0;
+#pragma unroll
+      for (int r = 0; r < SEL_CLUSTER; ++r) n[r] = r < CL ? load_remote(block + 31 - lane, r) : 0;
+#pragma unroll
+      for (int r = 0; r < SEL_CLUSTER; ++r) sum += n[r];
+      int before = warp_excl(sum, lane);
+      const int at = (__ffs(__ballot_sync(0xffffffffu, before < need && need <= before + sum)) - 1) & 31;
+      before = __shfl_sync(0xffffffffu, before, at);
+      const int d = (31 - at) * 64 + 63 - 2 * lane;  // two digits a lane, d and d - 1
+      int2 x[SEL_CLUSTER], c = make_int2(0, 0);
+#pragma unroll
+      for (int r = 0; r < SEL_CLUSTER; ++r) x[r] = r < CL ? load_remote2(hist + d - 1, r) : make_int2(0, 0);
+#pragma unroll
+      for (int r = 0; r < SEL_CLUSTER; ++r) {
+        c.x += x[r].x;
+        c.y += x[r].y;
+      }
+      before += warp_excl(c.x + c.y, lane);
+      if (before < need && need <= before + c.x + c.y) {  // one lane
+        const bool second = need > before + c.y;
+        sPick[0] = second ? d - 1 : d;
+        sPick[1] = need - before - (second ? c.y : 0);
+        sPick[2] = second ? c.x : c.y;
+      }
+    } else if (pass == 1) {  // for the third pass; nobody reads this buffer behind the barrier above
+      for (int i = threadIdx.x - 32; i < SEL_BINS; i += SEL_THREADS - 32) counts[0][i] = 0;
     }
     __syncthreads();
     prefix = prefix << bits | (uint32_t)sPick[0];
@@ -1188,7 +1199,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
     kb += tot[r].x;
     tb += tot[r].y;
   }
-  sm100::cluster_sync();  // no CTA leaves while another reads its counts
+  sm100::cluster_arrive();  // no CTA leaves while another reads its counts
   for (int q = 0; q < rounds; ++q) {
     const int p = cb + q * SEL_ROUND + (warp * 32 + lane) * KPT;
     if (!once) {
@@ -1216,6 +1227,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
       t += tied;
     }
   }
+  sm100::cluster_wait();
 }
 
 // Kept rows into the new cache, a token block at a time: one CTA per (block, K or V and head, sequence).
