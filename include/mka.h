@@ -333,8 +333,8 @@ MKA_API int mka_kv8_append(const mka_kv8_config* cfg, const mka_kv8_cache* cache
                            int64_t row_stride, int64_t batch_stride, int32_t n, const int32_t* pos, const int32_t* count,
                            void* stream);
 /* Values (dtype) of positions first[b] (NULL: 0) .. first[b] + rows[b] - 1 (rows NULL: n; clamped to
- * [0, n]) to rows 0.. of k_out, v_out, addressed like k_new of mka_kv8_append; other rows are left as
- * they were.  A range outside the cache records MKA_ERR_DEVICE_BOUNDS and reads nothing. */
+ * [0, n]) to rows 0.. of k_out, v_out, addressed like k_new of mka_kv8_append (batch_stride 0 only with one
+ * sequence); other rows are left as they were.  A range outside the cache records MKA_ERR_DEVICE_BOUNDS and reads nothing. */
 MKA_API int mka_kv8_read(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const int32_t* first, const int32_t* rows,
                          int32_t n, void* k_out, void* v_out, int64_t row_stride, int64_t batch_stride, void* stream);
 /* Bytes of scratch for mka_kv8_attention with n new tokens (0 on a bad cfg). */

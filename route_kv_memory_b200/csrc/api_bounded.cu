@@ -172,6 +172,7 @@ int mka_kv8_read(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const in
   if (!cache) return fail(MKA_ERR_INVALID_ARG, "%s: cache is NULL", __func__);
   TRY(check_kv8(__func__, cfg, cache, &kv));
   TRY(check_rows(__func__, kv, row_stride, batch_stride, n));
+  if (cfg->batch > 1 && batch_stride == 0) return fail(MKA_ERR_INVALID_ARG, "%s: the sequences' outputs are the same rows", __func__);
   NEED(k_out); NEED(v_out);
   TRY(check_positions(__func__, first, "first", false));
   TRY(check_positions(__func__, rows, "rows", false));
@@ -232,7 +233,7 @@ int mka_kv8_evict(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const i
   if (keep < 1 || first < 0 || recent < 0 || (int64_t)first + recent > keep)
     return fail(MKA_ERR_INVALID_ARG, "%s: keep must be >= 1 and first + recent within it", __func__);
   if (keep > d.a.Lmax) return fail(MKA_ERR_INVALID_ARG, "%s: keep exceeds the new cache", __func__);
-  if (cache->k == dst->k || cache->v == dst->v || cache->k_scale == dst->k_scale || cache->v_scale == dst->v_scale ||
+  if (cache->k == dst->k || cache->v == dst->v || cache->k == dst->v || cache->v == dst->k || cache->k_scale == dst->k_scale || cache->v_scale == dst->v_scale ||
       (const void*)weights == dst_weights || (const void*)lens == dst_lens)
     return fail(MKA_ERR_INVALID_ARG, "%s: dst must be another cache", __func__);
   TRY(check_positions(__func__, lens, "lens", true));

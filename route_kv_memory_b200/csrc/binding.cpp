@@ -21,6 +21,12 @@ struct Refused : std::runtime_error {  // becomes a ValueError
   using std::runtime_error::runtime_error;
 };
 struct Raised {};  // a Python exception is set
+// Lets other Python threads run during the call: a launch can wait for room in the stream's queue.  (The caller
+// holds the arguments.)
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // The C structure inside a ctypes structure.
 template <typename T>
@@ -170,6 +176,7 @@ int window_attention(PyObject* const* a) {  // c, q, k, v, lens, out, lse, strea
   const int32_t* pl = positions(lens, "lens", c.batch);
   float* ps = dense<float>(lse, "lse", at::kFloat, (long long)c.batch * c.n_q_heads * pad);
   void* s = call_stream(a[7], {q, k, v, lens, out, lse});
+  Unlocked unlocked;
   return mka_window_attention(&c, &st, q->data_ptr(), k->data_ptr(), v->data_ptr(), pl, out->data_ptr(), ps, s);
 }
 
@@ -189,6 +196,7 @@ int window_attention_backward(PyObject* const* a) {  // c, q, k, v, out, lse, do
   void* pv = dense(dv, "dv", at::kBFloat16, rows * c.n_kv_heads * c.d_head);
   const size_t n = bytes(*ws);
   void* s = call_stream(a[12], {q, k, v, out, lse, dout, lens, dq, dk, dv, ws});
+  Unlocked unlocked;
   return mka_window_attention_backward(&c, &st, q->data_ptr(), k->data_ptr(), v->data_ptr(), out->data_ptr(), ps,
                                        dout->data_ptr(), pl, pq, pk, pv, ws->data_ptr(), n, s);
 }
@@ -201,6 +209,7 @@ int kv8_append(PyObject* const* a) {  // c, cache, k_new, v_new, pos, count, str
   const Rows r = kv_rows(c, *k, *v, "k_new, v_new");
   const int32_t *pp = positions(pos, "pos", c.batch), *pc = positions(count, "count", c.batch);
   void* s = call_stream(a[6], {k, v, pos, count, x.t[0], x.t[1], x.t[2], x.t[3]});
+  Unlocked unlocked;
   return mka_kv8_append(&c, x.c, k->data_ptr(), v->data_ptr(), r.row, r.batch, r.n, pp, pc, s);
 }
 
@@ -212,6 +221,7 @@ int kv8_read(PyObject* const* a) {  // c, cache, first, rows, k_out, v_out, stre
   const Rows r = kv_rows(c, *k, *v, "k_out, v_out");
   const int32_t *pf = positions(first, "first", c.batch), *pr = positions(rows, "rows", c.batch);
   void* s = call_stream(a[6], {first, rows, k, v, x.t[0], x.t[1], x.t[2], x.t[3]});
+  Unlocked unlocked;
   return mka_kv8_read(&c, x.c, pf, pr, r.n, k->data_ptr(), v->data_ptr(), r.row, r.batch, s);
 }
 
@@ -228,6 +238,7 @@ int kv8_attention(PyObject* const* a) {  // c, cache, q, lens, out, weights, ws,
   float* pw = dense<float>(weights, "weights", at::kFloat, (long long)c.batch * c.n_kv_heads * c.max_positions);
   const size_t nb = bytes(*ws);
   void* s = call_stream(a[7], {q, lens, out, weights, ws, x.t[0], x.t[1], x.t[2], x.t[3]});
+  Unlocked unlocked;
   return mka_kv8_attention(&c, x.c, pq, n, pl, po, pw, ws->data_ptr(), nb, s);
 }
 
@@ -246,6 +257,7 @@ int kv8_evict(PyObject* const* a) {  // c, cache, lens, weights, keep, first, re
   int32_t* pk = dense<int32_t>(kept, "kept", at::kInt, heads * keep);
   const size_t nb = bytes(*ws);
   void* s = call_stream(a[13], {lens, w, lens2, w2, kept, ws, x.t[0], x.t[1], x.t[2], x.t[3], y.t[0], y.t[1], y.t[2], y.t[3]});
+  Unlocked unlocked;
   return mka_kv8_evict(&c, x.c, pl, pw, keep, first, recent, &d, y.c, pl2, pw2, pk, ws->data_ptr(), nb, s);
 }
 

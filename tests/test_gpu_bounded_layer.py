@@ -4,6 +4,7 @@ import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -156,6 +157,62 @@ for h in range(Hkv):
 assert new.lens.tolist() == [64] and kept[0, 0, :4].tolist() == [0, 1, 2, 3] and kept[0, 0, -1].item() == S - 1
 print("captured first: ok")
 """
+
+
+def steps_on(mka, seed, dh, stream):
+    """Training steps of window attention and steps of an 8-bit cache that is thinned, all on `stream`: the results."""
+    g, B, S, Hq, H, keep = torch.Generator().manual_seed(seed), 2, 300, 6, 2, 100
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g).bfloat16().cuda()
+
+    def zeros(*s, dtype=torch.bfloat16):
+        return torch.zeros(*s, dtype=dtype, device="cuda")
+    c = mka.make_attn_config(B, S, Hq, H, dh, window=70, sinks=2)
+    q, k, v, do, q4 = rnd(B, S, Hq, dh), rnd(B, S, H, dh), rnd(B, S, H, dh), rnd(B, S, Hq, dh), rnd(B, 4, Hq, dh)
+    out, dq, dk, dv, lse = zeros(B, S, Hq, dh), zeros(B, S, Hq, dh), zeros(B, S, H, dh), zeros(B, S, H, dh), mka.attention_lse(c)
+    lens = torch.tensor([S, 211], dtype=torch.int32, device="cuda")
+    ws = mka.buffer(mka.mka_window_attention_backward_workspace_size(c))
+    c8, d8 = mka.make_kv8_config(B, S + 8, Hq, H, dh), mka.make_kv8_config(B, keep, Hq, H, dh)
+    a, d = (mka.kv8_cache(*[zeros(B, H, n, dh, dtype=torch.uint8) for _ in "kv"],
+                          *[zeros(B, H, -(-n // 64), dtype=torch.float32) for _ in "kv"]) for n in (S + 8, keep))
+    at, l2, kept = zeros(B, dtype=torch.int32), zeros(B, dtype=torch.int32), zeros(B, H, keep, dtype=torch.int32)
+    w, w2, o8 = zeros(B, H, S + 8, dtype=torch.float32), zeros(B, H, keep, dtype=torch.float32), zeros(B, 4, Hq, dh)
+    ko, vo = zeros(B, keep, H, dh), zeros(B, keep, H, dh)
+    ws8 = mka.buffer(mka.mka_kv8_attention_workspace_size(c8, 4, True))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(stream):
+            w.zero_()
+        mka.mka_window_attention(c, q, k, v, lens, out, lse, stream=stream)
+        mka.mka_window_attention_backward(c, q, k, v, out, lse, do, lens, dq, dk, dv, ws, stream=stream)
+        mka.mka_kv8_append(c8, a, k, v, at, stream=stream)
+        mka.mka_kv8_attention(c8, a, q4, lens, o8, w, ws8, stream=stream)
+        mka.mka_kv8_evict(c8, a, lens, w, keep, 3, 20, d8, d, l2, w2, kept, ws8, stream=stream)
+        mka.mka_kv8_read(d8, d, None, l2, ko, vo, stream=stream)
+    stream.synchronize()
+    return [t.cpu() for t in (out, dq, dk, dv, o8, w, kept, w2, ko, vo)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dh", [64, 128])
+def test_two_threads_on_two_streams(mka, dh):
+    """Calls of two threads at once, each on a stream and with buffers of its own, give what they give alone."""
+    alone = [steps_on(mka, seed, dh, torch.cuda.current_stream()) for seed in (1, 2)]
+    got = [None, None]
+
+    def work(i, stream):
+        got[i] = steps_on(mka, i + 1, dh, stream)
+    threads = [threading.Thread(target=work, args=(i, torch.cuda.Stream())) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert got[i] is not None
+        for x, y in zip(alone[i], got[i]):
+            assert torch.equal(x, y)
+    assert mka.mka_status() == 0
 
 
 @pytest.mark.gpu

@@ -502,17 +502,19 @@ def test_bad_arguments(mka):
     assert lib.mka_kv8_append(c, mka.mka_kv8_cache(0x1000, 0x2000, None, 0x4000), a, a, 128, 1280, 10, a, None, None) == bad
     assert lib.mka_kv8_read(c, x, a2, None, 10, a, a, 128, 1280, None) == bad
     assert lib.mka_kv8_read(c, x, None, None, 10, a, odd, 128, 1280, None) == bad
+    assert lib.mka_kv8_read(c, x, None, None, 10, a, a, 128, 0, None) == bad  # both sequences to the same rows
     assert lib.mka_kv8_attention(c, x, a, 0, a, a, None, a, 1 << 40, None) == bad
     assert lib.mka_kv8_attention(c, x, a, 1, None, a, None, a, 1 << 40, None) == bad
     assert lib.mka_kv8_attention(c, x, a, 1, a, a, a2, a, 1 << 40, None) == bad
     assert lib.mka_kv8_attention(c, x, a, 1, a, a, None, a, mka.mka_kv8_attention_workspace_size(c) - 1,
                                  None) == mka.MKA_ERR_WORKSPACE
     assert mka.mka_kv8_attention_workspace_size(c, 1, True) > mka.mka_kv8_attention_workspace_size(c, 1)
-    y, l2, w2 = fake(mka, 0x9000), ctypes.c_void_p(0x2000), ctypes.c_void_p(0x3000)
+    y, l2, w2, crossed = fake(mka, 0x9000), ctypes.c_void_p(0x2000), ctypes.c_void_p(0x3000), fake(mka, 0x2000)
+    crossed.k, crossed.v = x.v, x.k
 
     def ev(c2=None, cache=x, dst=y, lens=a, w=a, keep=10, first=2, recent=3, dl=l2, dw=w2, kept=a, ws=a, n=1 << 20):
         return lib.mka_kv8_evict(c, cache, lens, w, keep, first, recent, c2 or cfg(mka), dst, dl, dw, kept, ws, n, None)
-    for kw in ({"dst": x}, {"dst": None}, {"lens": None}, {"w": None}, {"keep": 0}, {"first": -1}, {"recent": 9}, {"dl": None},
+    for kw in ({"dst": x}, {"dst": crossed}, {"dst": None}, {"lens": None}, {"w": None}, {"keep": 0}, {"first": -1}, {"recent": 9}, {"dl": None},
                {"dl": a}, {"dw": a}, {"kept": None}, {"ws": None}, {"keep": 301}, {"c2": cfg(mka, batch=3)},
                {"c2": cfg(mka, n_kv_heads=1)}, {"c2": cfg(mka, d_head=128)}, {"c2": cfg(mka, max_positions=9)}):
         assert ev(**kw) == bad, kw
