@@ -1002,16 +1002,20 @@ __global__ void sink_sum_kernel(AttnBwdArgs a) {
 
 constexpr int PLAN_BINS = 128;  // lengths of dK/dV items told apart
 // WN: dsum[(b * Hq + h) * ld + t] = sum_i dO * O over head h of token t, 0 for t >= lens[b] up to ld.
-// A warp per (token, 32 pieces of 16 bytes): 2 (d_head 128) or 4 heads; any row strides.
-__global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
+// A warp takes DS tokens and 32 pieces of 16 bytes of each (2 heads of 128 or 4 of 64), all loads in flight, and
+// writes the DS sums of a head next to each other; any row strides.  2 x 4096 with 1006 rows in use in the
+// second, 28 heads of 128: 16 us (a warp per token, its loads in turn and its sums scattered: 21 us; 8 tokens a warp:
+// as fast there, slower for few tokens).
+constexpr int DS = 4;
+__global__ void __launch_bounds__(256, 3) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
                                                           const bf16* __restrict__ o, int ld_o, AttnBwdArgs a,
                                                           float* __restrict__ dsum) {
   wait_previous_kernel();
   allow_next_kernel();
   const int lane = threadIdx.x & 31, per = a.dh / 8, pieces = a.Hq * per;
-  const long long tok = ((long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x) >> 5;
-  if (blockIdx.x == 0) {  // the plan: counters, and the items of dK/dV that have steps, longest first
+  if (blockIdx.x == 0) {  // the plan (one block): counters, and the items of dK/dV that have steps, longest first
     __shared__ int at[PLAN_BINS];
+    if (blockIdx.y) return;
     const int n = kv_items(a);
     int sh = 0;  // lengths are told apart in steps of 2^sh query tiles
     while (((a.S + BT - 1) / BT >> sh) >= PLAN_BINS) ++sh;
@@ -1045,26 +1049,50 @@ __global__ void __launch_bounds__(256) window_dsum_kernel(const bf16* __restrict
     }
     return;
   }
-  if (tok >= (long long)a.B * a.lse_ld) return;
-  const int b = (int)(tok / a.lse_ld), t = (int)(tok % a.lse_ld);
-  const bool in = t < used_rows(a, b);
-  const uint4* x = (const uint4*)(dout + ((size_t)b * a.S + t) * (size_t)ld_do);
-  const uint4* y = (const uint4*)(o + ((size_t)b * a.S + t) * (size_t)ld_o);
-  for (int p = lane; p - lane < pieces; p += 32) {
-    float acc = 0.f;
-    if (in && p < pieces) {
-      const uint4 u = x[p], v = y[p];
-      const __nv_bfloat162* u2 = (const __nv_bfloat162*)&u;
-      const __nv_bfloat162* v2 = (const __nv_bfloat162*)&v;
+  const int group = blockIdx.x - 1, p = blockIdx.y * 256 + threadIdx.x;
+  if (p - lane >= pieces) return;
+  const int b = group / (a.lse_ld / DS), t0 = group % (a.lse_ld / DS) * DS;
+  const int in = used_rows(a, b) - t0, px = min(p, pieces - 1) * 8;  // in: tokens in use of the DS
+  const bf16* x = dout + ((size_t)b * a.S + t0) * (size_t)ld_do + px;
+  const bf16* y = o + ((size_t)b * a.S + t0) * (size_t)ld_o + px;
+  float acc[DS];
+#pragma unroll
+  for (int i = 0; i < DS; ++i) acc[i] = 0.f;
+  if (in > 0) {
+    uint4 u[DS], v[DS];
+#pragma unroll
+    for (int i = 0; i < DS; ++i) {
+      u[i] = *(const uint4*)(x + (size_t)min(i, in - 1) * ld_do);
+      v[i] = *(const uint4*)(y + (size_t)min(i, in - 1) * ld_o);
+    }
+#pragma unroll
+    for (int i = 0; i < DS; ++i) {
+      const __nv_bfloat162* u2 = (const __nv_bfloat162*)&u[i];
+      const __nv_bfloat162* v2 = (const __nv_bfloat162*)&v[i];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 fu = __bfloat1622float2(u2[e]), fv = __bfloat1622float2(v2[e]);
-        acc = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc));
+        acc[i] = fmaf(fu.x, fv.x, fmaf(fu.y, fv.y, acc[i]));
       }
+      if (i >= in) acc[i] = 0.f;
     }
-    for (int k = per / 2; k > 0; k >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, k);
-    if (lane % per == 0 && p < pieces) dsum[((size_t)b * a.Hq + p / per) * a.lse_ld + t] = acc;
   }
+  // Sums over the head's 16 (8) lanes: steps that each hand half of the tokens to the other lane, until a lane is
+  // left with one token's, then plain ones over the lanes that share the token
+  int k = per / 2, tok = 0;
+#pragma unroll
+  for (int n = DS / 2; n > 0; n >>= 1, k >>= 1) {
+    const bool up = lane & k;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? acc[i] : acc[i + n], k);
+      acc[i] = (up ? acc[i + n] : acc[i]) + other;
+    }
+    tok += up ? n : 0;
+  }
+  const int share = 2 * k - (k > 0);  // lane bits of the lanes that share a token
+  for (; k > 0; k >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], k);
+  if (p < pieces && (lane & share) == 0) dsum[((size_t)b * a.Hq + p / per) * a.lse_ld + t0 + tok] = acc[0];
 }
 
 }  // namespace tcb
@@ -1154,8 +1182,8 @@ cudaError_t window_attention_backward_tc(const AttnBwdArgs& args, const AttnBwdS
       a.sinks < 0 || a.sinks > a.S || a.window > a.S || (long long)a.B * a.S >= (1LL << 31))
     return cudaErrorInvalidValue;
   a.dsum = dsum;
-  const long long warps = (long long)a.B * a.lse_ld;
-  cudaError_t e = launch_dependent(tcb::window_dsum_kernel, (unsigned)(1 + (warps * 32 + 255) / 256), 256, 0, s,
+  const dim3 dgrid(1 + a.B * (a.lse_ld / tcb::DS), (a.Hq * (a.dh / 8) + 255) / 256);
+  cudaError_t e = launch_dependent(tcb::window_dsum_kernel, dgrid, 256, 0, s,
                                    (const bf16*)a.dout, ld.dout, (const bf16*)o, ld.o, a, dsum);
   CUtensorMap tq, tdo, tk, tv;
   const int rows = a.B * a.S;
