@@ -76,7 +76,9 @@ CASES = [
     (1, 129, 7, 1, 128, 64, 4), (1, 255, 4, 2, 64, 64, 4), (2, 256, 4, 1, 128, 129, 3), (1, 300, 4, 2, 64, 0, 5),
     (1, 300, 4, 2, 128, 300, 0), (1, 385, 2, 1, 64, 127, 130), (1, 513, 4, 4, 128, 100, 128), (1, 640, 3, 1, 64, 1, 300),
     (1, 1400, 4, 2, 64, 1024, 4), (1, 1300, 3, 1, 128, 1100, 140), (2, 1200, 2, 1, 128, 1025, 0),
-    (3, 390, 4, 2, 64, 255, 4), (1, 1100, 8, 2, 128, 256, 4), (1, 1537, 2, 1, 64, 5, 2),
+    (3, 390, 4, 2, 64, 255, 4), (1, 1100, 8, 2, 128, 256, 4), (1, 1537, 2, 1, 64, 5, 2), (2, 200, 5, 1, 64, 60, 2),
+    # more query tiles than SMs: two of them in an item, with odd groups also two of different rows
+    (1, 700, 28, 4, 128, 200, 3), (2, 1300, 9, 3, 64, 1030, 2), (1, 1000, 24, 8, 128, 0, 0), (1, 641, 32, 8, 64, 90, 140),
 ]
 
 
@@ -92,6 +94,7 @@ def test_against_definition(mka, case):
 @pytest.mark.parametrize("case,lens", [
     ((3, 300, 4, 2, 64, 70, 4), [300, 0, 129]), ((4, 260, 2, 1, 128, 128, 1), [1, 256, 257, 128]),
     ((2, 700, 4, 2, 128, 64, 140), [700, 333]), ((2, 1300, 2, 1, 64, 1030, 3), [1300, 1153]), ((3, 513, 2, 2, 64, 0, 0), [513, 384, 2]),
+    ((3, 700, 10, 2, 64, 130, 5), [700, 0, 401]), ((2, 1300, 7, 1, 128, 1040, 1), [640, 1300]),
 ])
 def test_padded_batch(mka, case, lens):
     """Padding rows hold NaN and infinities: they reach nothing, and nothing is written there."""
