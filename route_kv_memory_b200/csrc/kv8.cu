@@ -1233,23 +1233,25 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const float* weight
 // Kept rows into the new cache, a token block at a time: one CTA per (block, K or V and head, sequence).
 // The largest magnitude is found on the codes themselves (their low 7 bits order like the values), a
 // chunk at a time with its own scale, and codes whose scale stays are copied as they are.  Rows come one by
-// one (128 bytes): 8 heads, 8192 rows: 34 MB in about 9 us, bound by the chain lens - kept - code.
+// one (128 bytes): 8 heads, 8192 rows: 34 MB in about 9 us, bound by the chain kept - code.
 template <int DH, int CH>
-__global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args d, const int* kept, int keep, const int* lens2,
+__global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args d, const int* kept, int keep,
                                                       const float* weights, float* weights2) {
   __shared__ float red[AP_THREADS / 32];
   constexpr int CPR = DH / 16;
   const int b = blockIdx.z, kv = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
   allow_next_kernel();
   wait_previous_kernel();
-  const int t0 = blockIdx.x * d.block, rows = min(d.block, lens2[b] - t0);
-  if (rows <= 0) return;
+  // (`kept` is -1 behind a short sequence's positions: dst_lens need not be read first)
+  const int t0 = blockIdx.x * d.block, rows = min(d.block, keep - t0);
   const size_t hd = (size_t)b * a.Hkv + g;
   const uint8_t* src = (const uint8_t*)(kv ? a.v : a.k) + hd * a.Lmax * DH;
   const float* ss = (kv ? a.vs : a.ks) + hd * a.nblk;
   uint8_t* dst = (uint8_t*)(kv ? d.v : d.k) + (hd * d.Lmax + t0) * DH;
-  if (!kv && weights2 && threadIdx.x < rows)
-    weights2[hd * d.Lmax + t0 + threadIdx.x] = weights[hd * a.Lmax + kept[hd * keep + t0 + threadIdx.x]];
+  if (!kv && weights2 && threadIdx.x < rows) {
+    const int from = kept[hd * keep + t0 + threadIdx.x];
+    if (from >= 0) weights2[hd * d.Lmax + t0 + threadIdx.x] = weights[hd * a.Lmax + from];
+  }
   int j[CH];
   uint4 v[CH];
   float sc[CH], m = 0.f;
@@ -1285,7 +1287,7 @@ __global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args 
       if (exp_of(sc[i]) != e) v[i] = rescale16(v[i], exp_of(sc[i]) - e);
       *(uint4*)(dst + (size_t)(i * AP_THREADS + threadIdx.x) * 16) = v[i];
     }
-  if (threadIdx.x == 0) (kv ? d.vs : d.ks)[hd * d.nblk + blockIdx.x] = pow2(e);
+  if (threadIdx.x == 0 && j[0] >= 0) (kv ? d.vs : d.ks)[hd * d.nblk + blockIdx.x] = pow2(e);
 }
 
 // Calls f(integral_constant) with the 16-value chunks per thread of a token block.
@@ -1428,7 +1430,7 @@ cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, i
     constexpr int DH = decltype(dh)::value;
     return kv8::with_chunks(d.block, DH, [&](auto ch) {
       return launch_dependent(kv8::compact_kernel<DH, decltype(ch)::value>, grid, kv8::AP_THREADS, 0, s, a, d, (const int*)kept, keep,
-                              (const int*)lens2, weights, weights2);
+                              weights, weights2);
     });
   };
   return a.dh == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
