@@ -287,12 +287,16 @@ __device__ __forceinline__ Tiles unit_tiles(const Kv8Attn& a, int b) {
   t.n = t.len > 0 ? t.nsk + (t.len - 1) / TILE - t.lo + 1 : 0;
   return t;
 }
+// a / b of non-negative numbers; 64-bit divisions, a microsecond in a chain of them, only where they are needed.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 struct Split {  // `total` tiles over `grid` CTAs: the first `more` of them take one tile more than the others
   long long base, more;
-  __device__ __forceinline__ Split(long long total, int grid) : base(total / grid), more(total % grid) {}
+  __device__ __forceinline__ Split(long long total, int grid) : base(quotient(total, grid)), more(total - base * grid) {}
   __device__ __forceinline__ long long start(long long cta) const { return cta * base + min(cta, more); }
   __device__ __forceinline__ int cta_of(long long tile) const {
-    return (int)(tile < more * (base + 1) ? tile / (base + 1) : more + (tile - more * (base + 1)) / base);
+    return (int)(tile < more * (base + 1) ? quotient(tile, base + 1) : more + quotient(tile - more * (base + 1), base));
   }
 };
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
@@ -369,11 +373,14 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
     for (int i = 0; i < 4; ++i)
       for (int k = 0; k < STAGES; ++k) mbar_init(&bars[i][k], 1);
     fence_barrier_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   wait_previous_kernel();
   allow_next_kernel();  // (not before: merge_kernel reads lens ahead of its own wait)
   // this CTA's range of tiles [w0, w1) and the sequence that w0 falls into
   long long total;
+  Split split(0, 1);
   {
     const int per = (a.c.B + AT_THREADS - 1) / AT_THREADS, b0 = min(threadIdx.x * per, a.c.B), b1 = min(b0 + per, a.c.B);
     long long own = 0;
@@ -392,7 +399,8 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
       if (i < warp) before += sScan[i];
       total += sScan[i];
     }
-    const long long w0 = Split(total, gridDim.x).start(blockIdx.x);
+    split = Split(total, gridDim.x);
+    const long long w0 = split.start(blockIdx.x);
     if (w0 >= before && w0 < before + own) {  // one thread at most
       long long left = w0 - before;
       int b = b0;
@@ -410,7 +418,6 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
     }
     __syncthreads();
   }
-  const Split split(total, gridDim.x);
   int todo = (int)(split.start(blockIdx.x + 1) - split.start(blockIdx.x)), b = sStart[0];
   if (todo == 0) return;
   Tiles ts = sTiles;
@@ -899,6 +906,8 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
     before += sCount[i][0];
     total += sCount[i][1];
   }
+  Records rec = {};
+  if (ts.n && row < R) rec = unit_records(a, RT, DH, grid, before, total, b, u, upb, ts.n);
   // every CTA waits, so that this kernel's end means the attention's too
   wait_previous_kernel();
   if constexpr (WT) {
@@ -916,7 +925,6 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
     for (int k = 0; k < PER; ++k) out[k] = from_f<T>(0.f);
     return;
   }
-  const Records rec = unit_records(a, RT, DH, grid, before, total, b, u, upb, ts.n);
   const int nrec = rec.n;
   if (nrec == 1) return;  // written whole by its CTA
   const size_t step = rec.step;
