@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  // MODE 2, 3: what follows up to the first item runs under the end of the kernel in front; the loader waits for
-  // that before it touches memory, and every other access follows from its copies (the first item worked out
-  // in front of the wait: 1 x 255, 4/2 heads, 10.8 -> 9.75 us)
+  // MODE 2, 3: what follows up to the first item runs under the end of the kernel in front; every role waits for
+  // that kernel before it touches memory (the first item worked out in front of the wait: 1 x 255, 4/2 heads,
+  // 10.8 -> 9.75 us)
   if constexpr (WN)
     if (threadIdx.x != 0) allow_next_kernel();  // (thread 0, the loader, behind its wait)
   // TMEM column of O_t and of S_t / P_t
@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp runs the role, converged; one elected lane issues)
+    if constexpr (WN) wait_previous_kernel();  // (so that no wait's limit counts the time of the kernel in front)
     int kvit = 0, pc[2] = {0, 0};
     bool ok = true;
     WWork ww = {};
@@ -657,6 +658,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // causal output rows start on 32-byte boundaries: one 32-byte store per 16 columns
     const bool o32 = !GA && ((uintptr_t)a.o & 31) == 0 && a.o_ld % 16 == 0 && a.o_bstride % 16 == 0;
     const uint64_t pol_out = policy_evict_first();  // output rows: written once, not read here
+    if constexpr (WN) wait_previous_kernel();
     int sit = 0;
     for (int rr = 0; WN || rr * (int)gridDim.x < nwork; ++rr) {
       const int w = WN ? 0 : snake_item(rr, gridDim.x, blockIdx.x, nwork);
