@@ -345,8 +345,9 @@ MKA_API size_t mka_kv8_attention_workspace_size(const mka_kv8_config* cfg, int32
  * [0, max_positions]; positions at or past it, and hidden ones, reach no result, whatever they hold.
  * weights (nullable) [B, Hkv, max_positions] float32: position j gets the softmax weight that the n
  * queries of the Hq / Hkv heads of its KV head gave it added; hidden positions are left as they were.
- * Scores, softmax and sums are float32; probabilities enter the product with V rounded to half
- * precision relative to the row's largest (float32 rows: to twice that many bits).
+ * Scores, softmax and sums are float32.  A probability enters the product with V rounded: off by 2^-11 of
+ * itself, or by 2^-34 of the row's largest (each with its V block's scale) where that is more (float32 rows:
+ * 2^-22, or 2^-45).
  * ws: 16-byte aligned scratch, used by one call at a time. */
 MKA_API int mka_kv8_attention(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const void* q, int32_t n,
                               const int32_t* lens, void* out, float* weights, void* ws, size_t ws_bytes, void* stream);

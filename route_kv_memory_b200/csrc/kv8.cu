@@ -254,7 +254,11 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
 // consecutive bytes that a lane loads of a token's row serve as its fragments without any transposition
 // (K: bytes 4w..4w+3 of its pieces are k-step w; V: byte pairs of two tokens, joined by prmt).
 // e4m3 to half is exact; q enters as half after a power-of-two scaling of its row (SPLIT, float32 q: as
-// high and low halves); P as half, relative to the row's running reference (SPLIT: high and low).
+// high and low halves); P as half, 2^HELD times its size relative to the row's running reference, so that
+// it is off by 2^-11 of itself at most down to 2^-23 of the reference, and by 2^-34 of the reference below
+// that: half's numbers end at 2^-24, and weights left out there would still be in the softmax's sum.  SPLIT
+// carries the rest of that rounding as a second half 2^LOW as large, against codes 2^-LOW as large (multiples
+// of 2^-20: exact): off by 2^-22 of itself, or 2^-45 of the reference.
 //
 // Every warp streams its own 32 tokens of each 128-token tile through its own two stages of shared
 // memory, filled by TMA (K and V, 32 rows each) with the 128-byte (d_head 64: 64-byte) swizzle: no
@@ -272,7 +276,12 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
 constexpr int AT_THREADS = 128;
 constexpr int TILE = 128;      // tokens per CTA step, 32 per warp
 constexpr int STAGES = 2;      // per warp
-constexpr float LAZY = 8.f;    // log2: the reference moves when it is exceeded by more
+// log2: the reference moves when it is exceeded by more than LAZY; P, held 2^HELD as large, stays below 2^15,
+// and the low half below 2^15 too (half a step of the high one, 2^4, times 2^LOW).  LAZY + HELD = 15 splits
+// half's range between rare moves and small weights: 8 + 7 / 6 + 9 / 4 + 11 take 106.3 / 106.8 / 108.3 us for
+// 16 sequences of up to 32768 with 4 new tokens, 32.0 each for 1 x 131072.
+constexpr float LAZY = 6.f, HELD = 9.f;
+constexpr int LOW = 11;
 
 struct Tiles {  // the 128-token tiles of a unit: tile i at i < nsk ? i : lo + i - nsk
   int len, lo, nsk, n;
@@ -319,6 +328,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
+  return *(const uint32_t*)&h;
+}
+__device__ __forceinline__ uint32_t times_h2(uint32_t u, float f) {  // both halves times f (exact where f is a power of two)
+  const __half2 h = __hmul2(*(const __half2*)&u, __float2half2_rn(f));
   return *(const uint32_t*)&h;
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t u) { return __half22float2(*(const __half2*)&u); }
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
             }
       }
       // scores in log2 units are s * f; two references per row, for the sum (ml) and, with the exponent
-      // ev of V's block scale added, for the products with V's codes (mu)
+      // ev of V's block scale added and HELD taken off, for the products with V's codes (mu)
       bool over = false;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -597,7 +610,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            over |= fmaxf(s[h][t][k], s[h][t][k + 2]) * (kf[h] * rf[t][k]) > fminf(ml[t][k], mu[t][k] - ev[h]) + LAZY;
+            over |= fmaxf(s[h][t][k], s[h][t][k + 2]) * (kf[h] * rf[t][k]) > fminf(ml[t][k], mu[t][k] + HELD - ev[h]) + LAZY;
       if (__any_sync(0xffffffffu, over)) {  // move the references to the tile's maxima
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -608,7 +621,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
             for (int h = 0; h < 2; ++h) {
               const float z = fmaxf(s[h][t][k], s[h][t][k + 2]), v = z == -INFINITY ? z : z * (kf[h] * rf[t][k]);
               x = fmaxf(x, v);
-              y = fmaxf(y, v + ev[h]);
+              y = fmaxf(y, v + (ev[h] - HELD));
             }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
             pf[h][t][i] = transpose8x8(hi);
             if constexpr (SPLIT) {
               const float2 f = unpack_h2(hi);
-              pl[h][t][i] = transpose8x8(pack_h2(y[0] - f.x, y[1] - f.y));
+              pl[h][t][i] = transpose8x8(pack_h2((y[0] - f.x) * (1 << LOW), (y[1] - f.y) * (1 << LOW)));
             }
           }
       // O^T += V^T P^T; channel tile m holds the channels 2m and 2m + 1 of each lane's piece; piece i is
@@ -712,9 +725,12 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
           const uint32_t y = __byte_perm(vr[2][m >> 1], vr[3][m >> 1], sel);
           const uint32_t a0 = e4m3x2_to_h2(x), a1 = e4m3x2_to_h2(x >> 16), a2 = e4m3x2_to_h2(y), a3 = e4m3x2_to_h2(y >> 16);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            mma16816(o[m][t], a0, a1, a2, a3, pf[h][t][0], pf[h][t][1]);
-            if constexpr (SPLIT) mma16816(o[m][t], a0, a1, a2, a3, pl[h][t][0], pl[h][t][1]);
+          for (int t = 0; t < NT; ++t) mma16816(o[m][t], a0, a1, a2, a3, pf[h][t][0], pf[h][t][1]);
+          if constexpr (SPLIT) {
+            const uint32_t l0 = times_h2(a0, pow2(-LOW)), l1 = times_h2(a1, pow2(-LOW)), l2 = times_h2(a2, pow2(-LOW)),
+                           l3 = times_h2(a3, pow2(-LOW));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(o[m][t], l0, l1, l2, l3, pl[h][t][0], pl[h][t][1]);
           }
         }
       }

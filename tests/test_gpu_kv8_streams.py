@@ -1,0 +1,109 @@
+"""Attention over the 8-bit cache where a block of threads streams many tiles: error against the 64-bit
+definition with a floor far below the smallest weight that counts, streams over several units and sequences,
+long joins, summed weights."""
+import math
+
+import pytest
+import torch
+
+import bounded_ref as ref
+
+
+@pytest.fixture(scope="module")
+def mka():
+    import route_kv_memory_b200 as m
+    return m
+
+
+def codes_of(x, scale, block):
+    """e4m3 codes of x [B, H, L, dh] under scales [B, H, blocks]."""
+    return (x / scale.repeat_interleave(block, 2)[:, :, :x.shape[2], None]).to(torch.float8_e4m3fn)
+
+
+def value_of(codes, scale, block):
+    """What the codes of one sequence and head stand for, in float64 on the CPU, and each position's scale."""
+    s = scale.cpu().double().repeat_interleave(block)[:codes.shape[0]]
+    return codes.cpu().double() * s[:, None], s
+
+
+def attend(mka, c, cache, q, lens, weights=None):
+    n = q.shape[1]
+    out = torch.full_like(q, 7.0)
+    ws = mka.buffer(mka.mka_kv8_attention_workspace_size(c, n, weights is not None))
+    ws.fill_(255)
+    mka.mka_kv8_attention(c, cache, q, lens, out, weights, ws)
+    torch.cuda.synchronize()
+    return out
+
+
+def decode(q, k, v, vs, p, window, sinks, scale, bf16):
+    """Query rows q [r, dh] at position p over k, v [L, dh] (float64; vs [L]: V's scales): out, weights [r, L] and the
+    bounds of their errors.
+
+    Scores are float32 sums of dh exact products (ds); 2^x is good to 2^-22 and its argument, below 2^7, to
+    2^-17; a lane adds up a few hundred positions at most: 2^-15 covers both.  P is rounded to half, 2^-11 of
+    itself or 2^-34 of the largest weight times V scale (float32 rows: 2^-22, 2^-45); the output once to its type."""
+    j = torch.arange(k.shape[0])
+    m = j <= p
+    if window:
+        m = m & ((j > p - window) | (j < sinks))
+    k, v, vs = k[m], v[m], vs[m]
+    s = q @ k.T * scale
+    w = torch.softmax(s, -1)
+    o = w @ v
+    ds = (k.shape[1] + 8) * 2.0 ** -24 * (q.abs() @ k.abs().T).amax(-1, keepdim=True) * scale + 2.0 ** -15
+    top = (w * vs).amax(-1, keepdim=True)
+    e = (2 * ds + (2.0 ** -11 if bf16 else 2.0 ** -22)) * (w @ v.abs())
+    e = e + (2.0 ** -34 if bf16 else 2.0 ** -45) * top * (v / vs[:, None]).abs().sum(0)
+    e = e + (ref.BF16 if bf16 else 2.0 ** -23) * (o.abs() + e)
+    full, bound = torch.zeros(q.shape[0], len(j), dtype=torch.float64), torch.zeros(q.shape[0], len(j), dtype=torch.float64)
+    full[:, m], bound[:, m] = w, 2 * ds * w
+    return o, full, e, bound
+
+
+def check(mka, c, cache, q, lens, out, units, w0=None, w1=None):
+    """The outputs (and added weights) of these (sequence, KV head) pairs."""
+    G, n = c.n_q_heads // c.n_kv_heads, q.shape[1]
+    scale = c.attn_scale if c.attn_scale > 0 else 1 / math.sqrt(c.d_head)
+    for b, g in units:
+        L = lens[b]
+        k, _ = value_of(cache.tensors[0][b, g, :L].view(torch.float8_e4m3fn), cache.tensors[2][b, g], c.block)
+        v, vs = value_of(cache.tensors[1][b, g, :L].view(torch.float8_e4m3fn), cache.tensors[3][b, g], c.block)
+        added, slack = torch.zeros(c.max_positions, dtype=torch.float64), torch.zeros(c.max_positions, dtype=torch.float64)
+        for i in range(n):
+            p = L - n + i
+            got = out[b, i, g * G:(g + 1) * G].cpu().double()
+            if p < 0:
+                assert (got == 0).all()
+                continue
+            o, w, e, ew = decode(q[b, i, g * G:(g + 1) * G].cpu().double(), k, v, vs, p, c.window, c.sinks, scale,
+                                 c.dtype == mka.MKA_BF16)
+            assert ((got - o).abs() <= e).all(), f"({b}, {g}) {float(((got - o).abs() / e).max()):.3g} times its bound"
+            added[:L] += w.sum(0)
+            slack[:L] += ew.sum(0)
+        if w0 is not None:
+            total = w0[b, g].cpu().double() + added
+            far = (w1[b, g].cpu().double() - total).abs()
+            assert (far <= slack + 2.0 ** -23 * total.abs()).all(), (b, g)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh,G", [(64, 2), (64, 12), (128, 2), (128, 12)])
+def test_weights_far_below_the_largest(mka, dtype, dh, G):
+    """One position takes all but 1e-5 of the weight, and its V is 0: the output is what the others give.  As many units as
+    CTAs, so that a warp's stream is a quarter of a sequence."""
+    B, H, L, block = 128, 4, 4096, 64
+    c = mka.make_kv8_config(B, L, G * H, H, dh, block=block, dtype=dtype, attn_scale=1 / dh)
+    g = torch.Generator("cuda").manual_seed(dh + G)
+    ones = torch.ones(B, H, L // block, device="cuda")
+    sk, sv = ones * 2.0 ** -8, ones * 2.0 ** -6
+    k = 0.25 * torch.randn(B, H, L, dh, generator=g, device="cuda")
+    v = torch.randn(B, H, L, dh, generator=g, device="cuda").abs() + 0.125
+    k[:, :, 0], v[:, :, 0] = 1.0, 0.0
+    cache = mka.kv8_cache(codes_of(k, sk, block), codes_of(v, sv, block), sk, sv)
+    q = torch.full((B, 1, G * H, dh), math.log(1e5 * L), device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    out = attend(mka, c, cache, q, lens)
+    check(mka, c, cache, q, [L] * B, out, [(0, 0), (1, 3), (63, 2), (127, 3)])
+    assert mka.mka_status() == 0
