@@ -866,8 +866,12 @@ __device__ __forceinline__ void add_weights(const Kv8Attn& a, int RT, int DH, in
         sum = warp_sum(L == -INFINITY ? sum : sum * ex2(L - all));
         L = all;
       }
-      // (a row that sees nothing: every score -inf, weighed 0 by any finite normaliser)
-      if (lane == 0) lse[r] = row >= R ? INFINITY : L == -INFINITY && sum == 0.f ? 0.f : L + log2f(sum);
+      // (a row that sees nothing: every score -inf, weighed 0 by any finite normaliser; a row whose normaliser is NaN:
+      // one so low that what the row sees is weighed infinitely, NaN below, and a hidden position still 0)
+      if (lane == 0) {
+        const float norm = L == -INFINITY && sum == 0.f ? 0.f : L + log2f(sum);
+        lse[r] = row >= R ? INFINITY : norm != norm ? -3e38f : norm;
+      }
     }
     __syncthreads();
     for (int r = 0; r < m; r += 4) {
@@ -882,7 +886,7 @@ __device__ __forceinline__ void add_weights(const Kv8Attn& a, int RT, int DH, in
   }
 #pragma unroll
   for (int k = 0; k < WG_TOKENS; ++k)
-    if (j[k] >= 0) a.weights[hd * a.c.Lmax + j[k]] += w[k];
+    if (j[k] >= 0) a.weights[hd * a.c.Lmax + j[k]] += finite_or_nan(w[k]);
 }
 
 // Joins the partial results of the query rows; a unit without tiles gives 0.  WPR warps per row: 8 (a CTA

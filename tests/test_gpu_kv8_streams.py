@@ -107,3 +107,53 @@ def test_weights_far_below_the_largest(mka, dtype, dh, G):
     out = attend(mka, c, cache, q, lens)
     check(mka, c, cache, q, [L] * B, out, [(0, 0), (1, 3), (63, 2), (127, 3)])
     assert mka.mka_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [400, 70000])  # 400: a unit in a few blocks of threads; 70000: in several hundred
+@pytest.mark.parametrize("what", ["query 0", "query 2", "last key"])
+def test_summed_weights_beside_a_nan(mka, L, what):
+    """A query whose scores are NaN gives NaN to the positions that it sees and nothing to the others: hidden positions
+    keep their totals, and those that only other queries see get theirs."""
+    B, H, G, dh, n, block, window, sinks = 1, 2, 2, 64, 3, 64, L - 250, 2
+    c = mka.make_kv8_config(B, L, G * H, H, dh, block=block, window=window, sinks=sinks)
+    g = torch.Generator("cuda").manual_seed(L)
+    s = torch.full((B, H, -(-L // block)), 2.0 ** -6, device="cuda")
+    cache = mka.kv8_cache(*(codes_of(torch.randn(B, H, L, dh, generator=g, device="cuda"), s, block) for _ in "kv"), s, s.clone())
+    q = torch.randn(B, n, G * H, dh, generator=g, device="cuda").to(torch.bfloat16)
+    bad = 2  # the query whose scores are NaN
+    if what == "last key":
+        cache.tensors[0].view(torch.uint8)[:, :, L - 1] = 0x7f
+    else:
+        bad = int(what[-1])
+        q[0, bad] = math.nan
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    w0 = torch.rand(B, H, L, generator=g, device="cuda")
+    w1 = w0.clone()
+    out = attend(mka, c, cache, q, lens, w1)
+    seen = torch.zeros(n, L, dtype=torch.bool)
+    for i in range(n):
+        p = L - n + i
+        seen[i, p - window + 1:p + 1] = True
+        seen[i, :sinks] = True
+    w1, w0 = w1.cpu(), w0.cpu()
+    for h in range(H):
+        assert torch.equal(torch.isnan(w1[0, h]), seen[bad])
+        assert torch.equal(w1[0, h, ~seen.any(0)], w0[0, h, ~seen.any(0)])
+    finite = seen.any(0) & ~seen[bad]
+    assert finite.any()
+    good = [i for i in range(n) if i != bad]
+    assert torch.isnan(out[0, bad]).all() and torch.isfinite(out[0, good]).all()
+    # the positions that the NaN query does not see: what the others give
+    for h in range(H):
+        k, _ = value_of(cache.tensors[0][0, h], s[0, h], block)
+        v, vs = value_of(cache.tensors[1][0, h], s[0, h], block)
+        k = torch.nan_to_num(k)
+        total, slack = w0[0, h].double(), torch.zeros(L, dtype=torch.float64)
+        for i in good:
+            _, w, _, ew = decode(q[0, i, h * G:(h + 1) * G].cpu().double(), k, v, vs, L - n + i, window, sinks, dh ** -0.5, True)
+            total += w.sum(0)
+            slack += ew.sum(0)
+        far = (w1[0, h].double() - total).abs()
+        assert (far <= slack + 2.0 ** -23 * total)[finite].all()
+    assert mka.mka_status() == 0
