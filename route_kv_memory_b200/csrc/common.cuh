@@ -114,7 +114,9 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // front of it in the stream has finished, as soon as all of that one's CTAs have called
 // allow_next_kernel() or left.  It calls wait_previous_kernel(), which returns when the kernel in front
 // has finished and its writes are visible, before it touches memory that others may use, and in every
-// CTA, so that its own end means that everything in front has ended too.  Two kernels do work ahead of
+// CTA, so that its own end means that everything in front has ended too.  Its loads are ordinary ones (no
+// __ldg, no const __restrict__ operands): the read-only path wants data that stays unchanged from the kernel's
+// start, which may lie before the writes of the kernel in front.  Two kernels do work ahead of
 // that wait (kv8.cu's merge, tc_attention_bwd.cu's windowed dQ); the kernels that they follow call
 // allow_next_kernel() only behind their own wait.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(256) read_kernel(Kv8Args a, const int* first, 
   for (int i = 0; i < NC; ++i) {
     const int row = (at + i * 256) / CPR;
     if (row < r) {
-      v[i] = __ldg((const uint4*)(codes + (size_t)row * DH + ch * 16));
-      s[i] = __ldg(sc + ((f + row) >> a.lb));
+      v[i] = *(const uint4*)(codes + (size_t)row * DH + ch * 16);
+      s[i] = sc[(f + row) >> a.lb];
     }
   }
 #pragma unroll
@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int tb = min((ts.tile(first + it) * TILE + warp * 32 + 16 * h) >> a.c.lb, a.c.nblk - 1);
-        nks[h] = __ldg(ksc + tb);
-        nvs[h] = __ldg(vsc + tb);
+        nks[h] = ksc[tb];
+        nvs[h] = vsc[tb];
       }
     };
     load_scales(0);
@@ -1291,8 +1291,8 @@ __global__ void __launch_bounds__(AP_THREADS) compact_kernel(Kv8Args a, Kv8Args 
 #pragma unroll
   for (int i = 0; i < CH; ++i)
     if (j[i] >= 0) {
-      v[i] = __ldg((const uint4*)(src + (size_t)j[i] * DH + (i * AP_THREADS + threadIdx.x) % CPR * 16));
-      sc[i] = __ldg(ss + (j[i] >> a.lb));
+      v[i] = *(const uint4*)(src + (size_t)j[i] * DH + (i * AP_THREADS + threadIdx.x) % CPR * 16);
+      sc[i] = ss[j[i] >> a.lb];
     }
 #pragma unroll
   for (int i = 0; i < CH; ++i)

@@ -1007,9 +1007,8 @@ constexpr int PLAN_BINS = 128;  // lengths of dK/dV items told apart
 // second, 28 heads of 128: 16 us (a warp per token, its loads in turn and its sums scattered: 21 us; 8 tokens a warp:
 // as fast there, slower for few tokens).
 constexpr int DS = 4;
-__global__ void __launch_bounds__(256, 3) window_dsum_kernel(const bf16* __restrict__ dout, int ld_do,
-                                                          const bf16* __restrict__ o, int ld_o, AttnBwdArgs a,
-                                                          float* __restrict__ dsum) {
+__global__ void __launch_bounds__(256, 3) window_dsum_kernel(const bf16* dout, int ld_do, const bf16* o, int ld_o,
+                                                          AttnBwdArgs a, float* dsum) {
   wait_previous_kernel();
   allow_next_kernel();
   const int lane = threadIdx.x & 31, per = a.dh / 8, pieces = a.Hq * per;
