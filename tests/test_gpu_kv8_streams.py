@@ -157,3 +157,73 @@ def test_summed_weights_beside_a_nan(mka, L, what):
         far = (w1[0, h].double() - total).abs()
         assert (far <= slack + 2.0 ** -23 * total)[finite].all()
     assert mka.mka_status() == 0
+
+
+def grown(kind, B, H, L, dh, block, g):
+    """A cache's codes and scales.  "plain": blocks of different size; "rising": keys that grow along the sequence, so that
+    the softmax's reference moves from tile to tile, and values that shrink; "falling": the other way round."""
+    nb = -(-L // block)
+    k, v = (torch.randn(B, H, L, dh, generator=g, device="cuda") for _ in "kv")
+    at = torch.arange(nb, device="cuda") / nb
+    step = {"plain": torch.zeros(nb, device="cuda"), "rising": at, "falling": 1 - at}[kind]
+    jump = torch.randint(-1, 2, (2, B, H, nb), generator=g, device="cuda")
+    sk = torch.exp2((-7 + torch.floor(3 * step)).expand(B, H, nb) + (jump[0] if kind == "plain" else 0))
+    sv = torch.exp2((-7 - torch.floor(6 * step)).expand(B, H, nb) + jump[1])
+    wide = lambda s: s.repeat_interleave(block, 2)[:, :, :L, None] * 2.0 ** 6  # noqa: E731
+    sk, sv = sk.contiguous(), sv.contiguous()
+    return codes_of(k * wide(sk), sk, block), codes_of(v * wide(sv), sv, block), sk, sv
+
+
+STREAMS = [
+    # B, L, Hq, H, dh, block, dtype, window, sinks, n, lens, kind, checked units (None: all)
+    # sequences of every length, empty ones between: CTAs go on to the next unit and sequence
+    (24, 3000, 16, 8, 128, 64, "bf16", 0, 0, 1, "spread", "plain", 30),
+    (24, 3000, 16, 8, 64, 16, "f32", 0, 0, 2, "spread", "plain", 30),
+    (24, 3000, 8, 8, 64, 128, "bf16", 0, 0, 3, "spread", "rising", 30),
+    (24, 3000, 16, 8, 128, 32, "f32", 0, 0, 1, "spread", "falling", 30),
+    # 21 query rows per KV head: two groups of rows, each a unit
+    (12, 3000, 28, 4, 128, 64, "bf16", 0, 0, 3, "spread", "rising", 20),
+    (24, 3000, 10, 5, 64, 64, "f32", 0, 0, 6, "spread", "plain", 20),
+    # windows with sinks: lists of tiles with a gap
+    (16, 6000, 16, 8, 64, 32, "bf16", 2500, 200, 3, "spread", "plain", 20),
+    (20, 6000, 8, 4, 128, 64, "f32", 2500, 20, 2, "spread", "rising", 20),
+    # as many units of a few tiles as CTAs of either residence: units that one CTA streams whole
+    (111, 256, 8, 4, 64, 64, "bf16", 0, 0, 1, "near", "plain", 30),
+    (37, 640, 24, 8, 128, 64, "bf16", 0, 0, 5, "near", "falling", 30),
+    # one unit in more ranges than a CTA's warps join at once (32 records each), and one among many short ones
+    (1, 40000, 2, 1, 64, 64, "bf16", 0, 0, 1, "full", "rising", None),
+    (1, 40000, 12, 1, 128, 64, "f32", 0, 0, 1, "full", "plain", None),
+    (70, 40000, 2, 1, 64, 64, "bf16", 0, 0, 1, "one", "falling", None),
+    (70, 40000, 2, 1, 128, 64, "f32", 0, 0, 1, "one", "rising", None),
+    (64, 5000, 4, 2, 64, 64, "bf16", 0, 0, 1, "one", "plain", None),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weighed", [False, True])
+@pytest.mark.parametrize("case", STREAMS)
+def test_streams(mka, case, weighed):
+    B, L, Hq, H, dh, block, dtype, window, sinks, n, how, kind, units = case
+    lens = {"spread": [0 if b % 5 == 3 else max(1, L - 211 * b % L) for b in range(B)],
+            "near": [L - 3 * b % 100 for b in range(B)], "full": [L] * B,
+            "one": [L if b == 30 else 1 + b % 2 for b in range(B)]}[how]
+    c = mka.make_kv8_config(B, L, Hq, H, dh, block=block, dtype=dtype, window=window, sinks=sinks)
+    g = torch.Generator("cuda").manual_seed(L + dh + B)
+    cache = mka.kv8_cache(*grown(kind, B, H, L, dh, block, g))
+    for b in range(B):  # rows behind a sequence's end hold NaN
+        for t in cache.tensors[:2]:
+            t.view(torch.uint8)[b, :, lens[b]:] = 0x7f
+    q = torch.randn(B, n, Hq, dh, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    at = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    w0 = torch.rand(B, H, L, generator=g, device="cuda") if weighed else None
+    w1 = w0.clone() if weighed else None
+    out = attend(mka, c, cache, q, at, w1)
+    pairs = [(b, h) for b in range(B) for h in range(H)]
+    if units:  # the longest and the last ones, and others spread over the batch
+        pairs = pairs[::-(-len(pairs) // units)] + [pairs[-1]]
+    check(mka, c, cache, q, lens, out, pairs, w0, w1)
+    assert not torch.isnan(out).any()
+    again = w0.clone() if weighed else None
+    assert torch.equal(out, attend(mka, c, cache, q, at, again))  # sums in a fixed order
+    assert not weighed or torch.equal(again, w1)
+    assert mka.mka_status() == 0
