@@ -1431,11 +1431,13 @@ cudaError_t kv8_attention(const Kv8Attn& a, int is_bf16, int* status, cudaStream
 
 cudaError_t kv8_evict(const Kv8Args& a, const int* lens, const float* weights, int keep, int first, int recent,
                       const Kv8Args& d, int* lens2, float* weights2, int* kept, cudaStream_t s) {
-  // CTAs per head: shares of 4096 positions, at most 8 (portable), and no more than about two CTAs per SM
-  // over all heads
-  int dev = 0, sms = 148, cl = 1;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  while (cl < kv8::SEL_CLUSTER && cl * 4096 < a.Lmax && cl * a.B * a.Hkv <= sms) cl *= 2;
+  // CTAs per head: as few as take a head in one round each, at most 8 (portable).  A CTA (1024 threads of 64
+  // registers) fills an SM, 148, 74, 33 and 15 clusters of 1, 2, 4 and 8 fit the card, and a second round costs
+  // more than idle SMs or a second wave do.  The call with 1 / 2 / 4 / 8 CTAs a head, in us: 16 heads of 16384
+  // positions 13.9 / 14.2 / 14.4 / -, of 65536 49.2 / 30.2 / 14.4 / 25.1; 64 heads of 32768 32.8 / 17.7 / 29.2 /
+  // 60.2; 32 heads of 131072 106 / 60 / 40 / 37; the other way round only at 256 heads of 131072, 198 / 199 / 231 / 209.
+  int cl = 1;
+  while (cl < kv8::SEL_CLUSTER && cl * kv8::SEL_ROUND < a.Lmax) cl *= 2;
   cudaError_t e = raise_max_smem(kv8::select_kernel, kv8::SEL_SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2] = {};

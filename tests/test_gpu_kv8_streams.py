@@ -227,3 +227,34 @@ def test_streams(mka, case, weighed):
     assert torch.equal(out, attend(mka, c, cache, q, at, again))  # sums in a fixed order
     assert not weighed or torch.equal(again, w1)
     assert mka.mka_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,L,keep", [(3, 1, 50001, 700), (1, 2, 32769, 32000), (2, 4, 16384, 16383), (9, 4, 131072, 999),
+                                        (2, 1, 131073, 5000), (5, 30, 16385, 64)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_kept_positions_of_every_cluster_size(mka, B, H, L, keep, ties):
+    """One to eight blocks of threads a head, shares that end inside a warp's, more clusters than the card holds."""
+    dh, first, recent = 64, 3, 21
+    c, c2 = mka.make_kv8_config(B, L, H, H, dh), mka.make_kv8_config(B, keep, H, H, dh)
+    empty = lambda n: mka.kv8_cache(*(torch.zeros(B, H, n, dh, dtype=torch.uint8, device="cuda") for _ in "kv"),  # noqa: E731
+                                    *(torch.ones(B, H, -(-n // 64), device="cuda") for _ in "kv"))
+    cache, d = empty(L), empty(keep)
+    g = torch.Generator("cuda").manual_seed(L + keep)
+    w = torch.rand(B, H, L, generator=g, device="cuda")
+    if ties:
+        w = torch.floor(4 * w) / 4
+    lens = torch.tensor([L - 1201 * b % L for b in range(B)], dtype=torch.int32, device="cuda")
+    lens2, kept = torch.zeros_like(lens), torch.full((B, H, keep), -7, dtype=torch.int32, device="cuda")
+    w2 = torch.full((B, H, keep), -9.0, device="cuda")
+    mka.mka_kv8_evict(c, cache, lens, w, keep, first, recent, c2, d, lens2, w2, kept,
+                      mka.buffer(mka.mka_kv8_evict_workspace_size(c, keep)))
+    assert mka.mka_status() == 0 and torch.equal(lens2, lens.clamp_max(keep))
+    at = torch.arange(L, device="cuda")
+    for b in range(B):
+        n = int(lens[b])
+        forced = (at < first) | (at >= n - recent)
+        order = w[b].double().masked_fill(forced, math.inf).masked_fill(at >= n, -math.inf).sort(dim=-1, descending=True, stable=True)[1]
+        want = order[:, :min(keep, n)].sort(-1)[0]
+        assert torch.equal(kept[b, :, :want.shape[1]].long(), want) and (kept[b, :, want.shape[1]:] == -1).all()
+        assert torch.equal(w2[b, :, :want.shape[1]], w[b].gather(1, want)) and (w2[b, :, want.shape[1]:] == -9).all()
