@@ -270,9 +270,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tbase = *tmem_slot;
   // MODE 2, 3: what follows up to the first item runs under the end of the kernel in front; every role waits for
   // that kernel before it touches memory (the first item worked out in front of the wait: 1 x 255, 4/2 heads,
-  // 10.8 -> 9.75 us)
-  if constexpr (WN)
-    if (threadIdx.x != 0) allow_next_kernel();  // (thread 0, the loader, behind its wait)
+  // 10.8 -> 9.75 us).  The kernel behind may start at once (the first call of any thread of a CTA counts for all of
+  // it): those that work ahead of their wait follow kernels of their own call, see launch_dependent.
+  if constexpr (WN) allow_next_kernel();
   // TMEM column of O_t and of S_t / P_t
 #define O_COL(t) (128u * (uint32_t)(t))
 #define S_COL(t) (256u + 128u * (uint32_t)(t))
@@ -454,10 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (!mbar_wait(&item_empty[done & 1], ((done >> 1) & 1) ^ 1, abort, status)) break;
           items[done & 1] = ww;
           mbar_arrive(&item_full[done & 1]);
-          if (done == 0) {
-            wait_previous_kernel();
-            allow_next_kernel();
-          }
+          if (done == 0) wait_previous_kernel();
           it = {ww.b, ww.h0, 0};
         } else {
           it = work_item(w, a.B, a.Hq, a.Hkv, npairs, a.chunk);
@@ -499,10 +496,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (!ok) break;
       }
-      if (WN && done == 0) {  // (a CTA without items must not end in front of it either)
-        wait_previous_kernel();
-        allow_next_kernel();
-      }
+      if (WN && done == 0) wait_previous_kernel();  // (a CTA without items must not end in front of it either)
       if (WN && mbar_wait(&item_empty[done & 1], ((done >> 1) & 1) ^ 1, abort, status)) {
         items[done & 1].b = -1;
         mbar_arrive(&item_full[done & 1]);
