@@ -1036,9 +1036,11 @@ cudaError_t attention_prefill_tc(const AttnArgs& a, int* status, cudaStream_t s)
     // (a window's items run side by side over a few windows of keys: one chunk of all streams)
     c.chunk = kv_bytes <= 0.5 * l2 || a.window ? NS : (want < 1 ? 1 : (want > NS ? NS : want));
   }
-  // Long windows: the masked steps apart, which slows those (serial chunks) and speeds the others.  1 x
-  // 32768, 32/8 heads, in turn: window 4096 2105 -> 2010 us, 1024 785 -> 775, 512 464 -> 496, 256 330 -> 390.
-  if (win && (a.window == 0 || a.window >= 1024))
+  // Long windows, and sequences without one: the masked steps apart, which slows those (serial chunks) and speeds the
+  // others.  Masks in the loop / apart, 32/8 heads, us: 1 x 32768, head size 128, window 256 369 / 377, 512 518 / 514,
+  // 1024 737 / 709, 4096 2146 / 2040; head size 64 315 / 332, 420 / 416, 616 / 604, 1745 / 1699; 2 x 4096 without a
+  // window 268 / 258 and 241 / 237; without one, head size 128, 1 x 256 9.2 / 9.8, 640 16.9 / 17.0, 777 21.2 / 20.6.
+  if (win && (a.window ? a.window >= 1024 : a.S >= 768))
     return a.dh == 128 ? launch_attn<128, 3>(tq, tk, tv, c, status, grid, s)
                        : launch_attn<64, 3>(tq, tk, tv, c, status, grid, s);
   if (win)
