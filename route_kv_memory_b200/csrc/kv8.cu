@@ -1358,8 +1358,10 @@ cudaError_t kv8_read(const Kv8Args& a, const int* first, const int* rows, int n,
                             (T*)v_out, row_stride, batch_stride, status);
   };
   // two chunks a thread once that still leaves every SM four blocks; fewer rows: more threads
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   auto with_nc = [&](auto type, auto dh) {
-    return (long long)chunks * 2 * a.Hkv * a.B >= 2 * 256 * 148 * 4 ? run(type, dh, std::integral_constant<int, 2>())
+    return (long long)chunks * 2 * a.Hkv * a.B >= 2 * 256 * 4LL * sms ? run(type, dh, std::integral_constant<int, 2>())
                                                                     : run(type, dh, std::integral_constant<int, 1>());
   };
   auto with_dh = [&](auto type) {
