@@ -17,13 +17,29 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmka.so")
 
-for _lib_file in (LIB_PATH, os.path.join(_PKG, "_binding.so")):
-    if not os.path.exists(_lib_file):
-        raise ImportError(f"{_lib_file} is missing: build it with `python route_kv_memory_b200/_build.py` "
-                          "(or __graft_entry__.build()); this package has no CPU fallback")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is missing: build it with `python route_kv_memory_b200/_build.py` "
+                      "(or __graft_entry__.build()); this package has no CPU fallback")
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _binding  # noqa: E402  (linked to the library just loaded; built with it)
+
+class _Binding:
+    """The functions of _binding.so, loaded at the first call of one: it is tied to the torch that it was built
+    against, and the layer, which goes through ctypes, is not."""
+
+    def __getattr__(self, name):
+        again = "build it with `python route_kv_memory_b200/_build.py`; the bounded-memory operators need it"
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise ImportError(f"_binding.so cannot be loaded ({e}): {again}") from e
+        if m.torch_version != torch.__version__:
+            raise ImportError(f"_binding.so was built against torch {m.torch_version}, not {torch.__version__}: {again}")
+        setattr(self, name, getattr(m, name))
+        return getattr(self, name)
+
+
+_native = _Binding()
 
 MKA_OK = 0
 MKA_ERR_INVALID_ARG = -1
@@ -284,7 +300,7 @@ def attention_lse(c: mka_attn_config, device="cuda") -> torch.Tensor:
 def mka_window_attention(c: mka_attn_config, q, k, v, lens, out, lse=None, stream=None) -> None:
     """q, out [B, S, Hq, dh] (or flat heads), k, v [B, S, Hkv, dh] bf16, row strides allowed; lens [B] int32
     or None; lse from attention_lse() or None."""
-    _check(_binding.window_attention(c, q, k, v, lens, out, lse, stream), "mka_window_attention")
+    _check(_native.window_attention(c, q, k, v, lens, out, lse, stream), "mka_window_attention")
 
 
 def mka_window_attention_backward_workspace_size(c: mka_attn_config) -> int:
@@ -293,7 +309,7 @@ def mka_window_attention_backward_workspace_size(c: mka_attn_config) -> int:
 
 def mka_window_attention_backward(c: mka_attn_config, q, k, v, out, lse, dout, lens, dq, dk, dv, ws, stream=None) -> None:
     """Gradients of sum(dout * out) after mka_window_attention(c, q, k, v, lens, out, lse): dq, dk, dv bf16, dense."""
-    _check(_binding.window_attention_backward(c, q, k, v, out, lse, dout, lens, dq, dk, dv, ws, stream),
+    _check(_native.window_attention_backward(c, q, k, v, out, lse, dout, lens, dq, dk, dv, ws, stream),
            "mka_window_attention_backward")
 
 
@@ -326,12 +342,12 @@ def kv8_cache(k, v, k_scale, v_scale) -> mka_kv8_cache:
 def mka_kv8_append(c: mka_kv8_config, cache: mka_kv8_cache, k_new, v_new, pos, count=None, stream=None) -> None:
     """k_new, v_new [B, n, Hkv, dh] of the configuration's type (row and batch strides allowed, the same for both);
     pos, count [B] int32 on the device."""
-    _check(_binding.kv8_append(c, cache, k_new, v_new, pos, count, stream), "mka_kv8_append")
+    _check(_native.kv8_append(c, cache, k_new, v_new, pos, count, stream), "mka_kv8_append")
 
 
 def mka_kv8_read(c: mka_kv8_config, cache: mka_kv8_cache, first, rows, k_out, v_out, stream=None) -> None:
     """Values of positions first[b] .. first[b] + rows[b] - 1 to k_out, v_out [B, n, Hkv, dh] (strides allowed)."""
-    _check(_binding.kv8_read(c, cache, first, rows, k_out, v_out, stream), "mka_kv8_read")
+    _check(_native.kv8_read(c, cache, first, rows, k_out, v_out, stream), "mka_kv8_read")
 
 
 def mka_kv8_attention_workspace_size(c: mka_kv8_config, n: int = 1, with_weights: bool = False) -> int:
@@ -341,7 +357,7 @@ def mka_kv8_attention_workspace_size(c: mka_kv8_config, n: int = 1, with_weights
 def mka_kv8_attention(c: mka_kv8_config, cache: mka_kv8_cache, q, lens, out, weights, ws, stream=None) -> None:
     """Attention of the last n positions: q, out [B, n, Hq, dh] (or flat heads), dense; lens [B] int32 on the device;
     weights [B, Hkv, max_positions] float32 or None."""
-    _check(_binding.kv8_attention(c, cache, q, lens, out, weights, ws, stream), "mka_kv8_attention")
+    _check(_native.kv8_attention(c, cache, q, lens, out, weights, ws, stream), "mka_kv8_attention")
 
 
 def mka_kv8_evict_workspace_size(c: mka_kv8_config, keep: int) -> int:
@@ -351,7 +367,7 @@ def mka_kv8_evict_workspace_size(c: mka_kv8_config, keep: int) -> int:
 def mka_kv8_evict(c: mka_kv8_config, cache: mka_kv8_cache, lens, weights, keep: int, first: int, recent: int,
                   dst_c: mka_kv8_config, dst: mka_kv8_cache, dst_lens, dst_weights, kept, ws, stream=None) -> None:
     """Keeps `keep` positions of every sequence and KV head (the first, the last, the heaviest) in another cache."""
-    _check(_binding.kv8_evict(c, cache, lens, weights, keep, first, recent, dst_c, dst, dst_lens, dst_weights, kept, ws,
+    _check(_native.kv8_evict(c, cache, lens, weights, keep, first, recent, dst_c, dst, dst_lens, dst_weights, kept, ws,
                               stream), "mka_kv8_evict")
 
 

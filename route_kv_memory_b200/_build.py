@@ -20,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmka.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_TORCH = os.path.join(BUILD, "binding_torch.txt")  # the torch version that BINDING was built against
 SOURCES = ["api.cu", "gemm.cu", "memory.cu", "attention.cu", "decode.cu", "noalloc.cu", "api_bounded.cu", "kv8.cu", "tc_gemm.cu", "tc_attention.cu", "block_sparse.cu", "tc_attention_bwd.cu", "backward.cu", "selftest.cu"]
 HEADERS = ["common.cuh", "kernels.h", "sm100.cuh"]
 
@@ -74,26 +75,38 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def binding_is_current(torch_version: str) -> bool:
+    """Whether BINDING is newer than its sources and was built against this torch."""
+    newest = max(os.path.getmtime(p) for p in (os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "mka.h")))
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < newest or not os.path.exists(BINDING_TORCH):
+        return False
+    with open(BINDING_TORCH) as f:
+        return f.read() == torch_version
+
+
 def _build_binding(force: bool) -> None:
     """_binding.so: argument marshalling against torch's headers, linked to libmka.so beside it."""
-    src = os.path.join(CSRC, "binding.cpp")
-    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "mka.h")))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    import importlib.metadata
+    version = importlib.metadata.version("torch")  # (without importing it: an up-to-date build takes no time)
+    if not force and binding_is_current(version):
         return
     import torch
+    src = os.path.join(CSRC, "binding.cpp")
     home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     tmp = BINDING + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-isystem" + p for p in inc), src, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMKA_TORCH_VERSION="{torch.__version__}"', *("-isystem" + p for p in inc), src, "-o", tmp,
            "-L" + PKG, "-l:libmka.so", "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_TORCH, "w") as f:
+        f.write(version)
 
 
 if __name__ == "__main__":
