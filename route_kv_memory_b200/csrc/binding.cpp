@@ -140,16 +140,19 @@ struct Rows {
 Rows kv_rows(const mka_kv8_config& c, const at::Tensor& k, const at::Tensor& v, const char* name) {
   const at::ScalarType type = c.dtype == MKA_BF16 ? at::kBFloat16 : at::kFloat;
   const int64_t width = (int64_t)c.n_kv_heads * c.d_head;
-  const auto s = k.sizes(), st = k.strides();
-  bool ok = k.scalar_type() == type && s.size() >= 3 && s[0] == c.batch;
-  if (ok && s.size() == 4) ok = s[2] == c.n_kv_heads && s[3] == c.d_head && st[3] == 1 && (c.n_kv_heads == 1 || st[2] == c.d_head);
-  else if (ok) ok = s.size() == 3 && s[2] == width && st[2] == 1;
-  if (!ok)
-    refuse(k, name, std::string(c10::toString(type)) + " [" + std::to_string(c.batch) + ", n, " + std::to_string(c.n_kv_heads) +
-                        ", " + std::to_string(c.d_head) + "] with contiguous rows");
-  if (v.scalar_type() != type || v.sizes() != s || v.strides() != st)
-    refuse(v, name, "two tensors of the same type, shape and strides");
-  return {to_i32(s[1], "n"), s[1] > 1 ? st[1] : width, c.batch > 1 ? st[0] : 0};
+  auto rows = [&](const at::Tensor& t) -> Rows {  // (the stride of a dimension of size 1 does not count)
+    const auto s = t.sizes(), st = t.strides();
+    bool ok = t.scalar_type() == type && s.size() >= 3 && s[0] == c.batch;
+    if (ok && s.size() == 4) ok = s[2] == c.n_kv_heads && s[3] == c.d_head && st[3] == 1 && (c.n_kv_heads == 1 || st[2] == c.d_head);
+    else if (ok) ok = s.size() == 3 && s[2] == width && st[2] == 1;
+    if (!ok)
+      refuse(t, name, std::string(c10::toString(type)) + " [" + std::to_string(c.batch) + ", n, " + std::to_string(c.n_kv_heads) +
+                          ", " + std::to_string(c.d_head) + "] with contiguous rows, two tensors of the same type, shape and strides");
+    return {to_i32(s[1], "n"), s[1] > 1 ? st[1] : width, c.batch > 1 ? st[0] : 0};
+  };
+  const Rows a = rows(k), b = rows(v);
+  if (a.n != b.n || a.row != b.row || a.batch != b.batch) refuse(v, name, "two tensors of the same type, shape and strides");
+  return a;
 }
 
 // Row stride of t [B, S, heads, dh] or [B, S, heads * dh] (see mka_attn_strides).

@@ -258,3 +258,38 @@ def test_kept_positions_of_every_cluster_size(mka, B, H, L, keep, ties):
         want = order[:, :min(keep, n)].sort(-1)[0]
         assert torch.equal(kept[b, :, :want.shape[1]].long(), want) and (kept[b, :, want.shape[1]:] == -1).all()
         assert torch.equal(w2[b, :, :want.shape[1]], w[b].gather(1, want)) and (w2[b, :, want.shape[1]:] == -9).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,n", [(1, 1), (1, 3), (2, 1)])
+def test_strides_of_single_rows_do_not_matter(mka, B, n):
+    """K and V that differ in nothing but the stride of a dimension of size 1 are rows of the same places."""
+    H, dh = 2, 64
+    c = mka.make_kv8_config(B, 40, 4, H, dh, block=16)
+    g = torch.Generator("cuda").manual_seed(3)
+    k = torch.randn(B, n, H, dh, generator=g, device="cuda").bfloat16()
+    v = torch.randn(B, n, H, dh, generator=g, device="cuda").bfloat16()
+    st = list(v.stride())
+    if B == 1:
+        st[0] += 4096
+    if n == 1:
+        st[1] += 512
+    odd = v.as_strided(v.shape, st)
+    assert odd.stride() != k.stride() and torch.equal(odd, v)
+    got = []
+    for x in (v, odd):
+        cache = mka.kv8_cache(*(torch.zeros(B, H, 40, dh, dtype=torch.uint8, device="cuda") for _ in "kv"),
+                              *(torch.ones(B, H, 3, device="cuda") for _ in "kv"))
+        mka.mka_kv8_append(c, cache, k, x, torch.zeros(B, dtype=torch.int32, device="cuda"))
+        ko, vo = torch.zeros_like(k), torch.zeros_like(k).as_strided(k.shape, st)
+        mka.mka_kv8_read(c, cache, None, None, ko, vo)
+        got.append([t.clone() for t in cache.tensors] + [ko, vo])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got[0][:4], got[1][:4]))
+    assert torch.equal(got[0][4], got[1][4]) and torch.equal(got[0][5], got[1][5]) and bool(got[0][5].any())
+    with pytest.raises(ValueError, match="same"):
+        wide = torch.zeros(2, 3, 2 * H, dh, device="cuda").bfloat16()[:, :, :H]
+        c2 = mka.make_kv8_config(2, 40, 4, H, dh, block=16)
+        cache = mka.kv8_cache(*(torch.zeros(2, H, 40, dh, dtype=torch.uint8, device="cuda") for _ in "kv"),
+                              *(torch.ones(2, H, 3, device="cuda") for _ in "kv"))
+        mka.mka_kv8_append(c2, cache, wide, wide.contiguous(), torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert mka.mka_status() == 0
