@@ -280,8 +280,8 @@ constexpr int STAGES = 2;      // per warp
 // and the low half below 2^15 too (half a step of the high one, 2^4, times 2^LOW).  LAZY + HELD = 15 splits
 // half's range between rare moves and small weights: 8 + 7 / 6 + 9 / 4 + 11 take 106.3 / 106.8 / 108.3 us for
 // 16 sequences of up to 32768 with 4 new tokens, 32.0 each for 1 x 131072.
-constexpr float LAZY = 6.f, HELD = 9.f;
-constexpr int LOW = 11;
+constexpr float LAZY = 6.f;
+constexpr int HELD = 9, LOW = 11;
 
 struct Tiles {  // the 128-token tiles of a unit: tile i at i < nsk ? i : lo + i - nsk
   int len, lo, nsk, n;
@@ -353,6 +353,16 @@ template <int DH> struct AtCfg {
   static constexpr int WARP = STAGES * 2 * HALF;  // a warp's stages: K, V
   static constexpr int SMEM = 4 * WARP + 1024;
 };
+
+// O of a row from the products' sum: / sum, * 2^(U - L), the references of the products and of the sum, U HELD low.
+// In two factors: V's scales reach down to 2^-120, and 2^x is 0 below 2^-126.
+struct Norm {
+  float a, b;
+  __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
+};
+__device__ __forceinline__ Norm row_norm(float L, float U, float sum) {
+  return {sum == 0.f ? 0.f : 1.f / (1 << HELD) / sum, sum == 0.f ? 0.f : sm100::ex2(U + (float)HELD - L)};  // nothing seen: 0
+}
 
 // NT: groups of 8 query rows; SPLIT: float32 queries and outputs; WT: raw scores go to a.scores.
 template <typename T, int DH, int NT, bool WT>
@@ -783,10 +793,10 @@ __global__ void __launch_bounds__(AT_THREADS, DH == 128 && NT == 2 ? 2 : 3)
         x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
       }
       if (whole) {
-        const float f = sum == 0.f ? 0.f : ex2(U - L) / sum;  // a row that sees nothing is 0
+        const Norm f = row_norm(L, U, sum);
         T* out = (T*)a.out + ((size_t)b * a.n + row / a.G) * (size_t)(a.c.Hkv * a.G * DH) +
                  (size_t)(g * a.G + row % a.G) * DH + d;
-        out[0] = from_f<T>(x.x * f); out[1] = from_f<T>(x.y * f); out[2] = from_f<T>(x.z * f); out[3] = from_f<T>(x.w * f);
+        out[0] = from_f<T>(f(x.x)); out[1] = from_f<T>(f(x.y)); out[2] = from_f<T>(f(x.z)); out[3] = from_f<T>(f(x.w));
         if (WT && d == 0) *(float2*)(a.stats + 2 * (hd * R + row)) = make_float2(L, sum);
       } else {
         float* rec = a.part + (slot * RT + r) * (DH + 4);
@@ -1002,9 +1012,9 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(Kv8Attn a, int RT, in
       for (int k = 0; k < PER; ++k) x[k] += sX[i][lane * PER + k] * f;
     }
   }
-  const float f = sum == 0.f ? 0.f : ex2(U - L) / sum;
+  const Norm f = row_norm(L, U, sum);
 #pragma unroll
-  for (int k = 0; k < PER; ++k) out[k] = from_f<T>(x[k] * f);
+  for (int k = 0; k < PER; ++k) out[k] = from_f<T>(f(x[k]));
 }
 
 // ============================================================================ eviction

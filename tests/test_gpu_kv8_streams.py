@@ -293,3 +293,24 @@ def test_strides_of_single_rows_do_not_matter(mka, B, n):
                               *(torch.ones(2, H, 3, device="cuda") for _ in "kv"))
         mka.mka_kv8_append(c2, cache, wide, wide.contiguous(), torch.zeros(2, dtype=torch.int32, device="cuda"))
     assert mka.mka_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [2.0 ** -114, 2.0 ** 112])
+@pytest.mark.parametrize("L", [100, 3000, 70000])  # one tile, whole and split units
+def test_values_near_the_ends_of_the_range(mka, dtype, size, L):
+    """V whose block scales are near the smallest and the largest, under nearly equal weights: the factor of the whole row is
+    then near the ends of float32's range too."""
+    H, dh, block = 2, 64, 16
+    c = mka.make_kv8_config(1, L, H, H, dh, block=block, dtype=dtype, attn_scale=2.0 ** -10)
+    g = torch.Generator("cuda").manual_seed(L)
+    nb = -(-L // block)
+    k, v = (torch.randn(1, H, L, dh, generator=g, device="cuda") for _ in "kv")
+    sk, sv = (torch.full((1, H, nb), 2.0 ** -6, device="cuda") for _ in "kv")
+    kc, vc = codes_of(k, sk, block), codes_of(v.abs(), sv, block)
+    cache = mka.kv8_cache(kc, vc, sk, sv * size)
+    q = torch.randn(1, 1, H, dh, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    out = attend(mka, c, cache, q, torch.full((1,), L, dtype=torch.int32, device="cuda"))
+    check(mka, c, cache, q, [L], out, [(0, h) for h in range(H)])
+    assert mka.mka_status() == 0
