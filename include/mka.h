@@ -302,7 +302,8 @@ MKA_API int mka_window_attention_backward(const mka_attn_config* cfg, const mka_
  * values are rounded to the nearest code (ties to even): to 2^-4 of the value, or 2^-10 of the block's
  * scale where that is more.  NaN and infinities are stored as NaN and do not enter the scale.  The
  * calls keep no lengths: every call is told the positions in use, in device memory, so sequences of
- * steps can be captured into a CUDA graph.  Position arrays hold int32 on the device. */
+ * steps can be captured into a CUDA graph.  Position arrays hold int32 on the device.  No output of a call
+ * may overlap another operand of it (out of mka_kv8_attention may be q). */
 typedef struct mka_kv8_config {
   int32_t batch;         /* B */
   int32_t max_positions; /* rows of the cache per sequence and head */

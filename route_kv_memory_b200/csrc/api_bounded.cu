@@ -4,6 +4,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "../../include/mka.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -36,6 +38,44 @@ int fail(int code, const char* fmt, ...) {
   do {              \
     if (p) NEED(p); \
   } while (0)
+
+// Operands of a call, checked last: an output may not overlap another operand.  (A kernel reads positions and kept
+// rows several times over; what it writes in between must not change them.)
+struct Span {
+  const char* name;
+  const void* p;  // null: not given
+  size_t bytes;
+  bool out;
+};
+int check_apart(const char* who, std::initializer_list<Span> spans) {
+  for (const Span* a = spans.begin(); a != spans.end(); ++a)
+    for (const Span* b = spans.begin(); b != a; ++b)
+      if ((a->out || b->out) && a->p && b->p && (uintptr_t)a->p < (uintptr_t)b->p + b->bytes &&
+          (uintptr_t)b->p < (uintptr_t)a->p + a->bytes)
+        return fail(MKA_ERR_INVALID_ARG, "%s: %s and %s overlap", who, b->name, a->name);
+  return MKA_OK;
+}
+// The same for operands of `rows` rows of bf16, some elements apart: they may lie in each other's gaps.
+struct RowSpan {
+  const char* name;
+  const void* p;
+  int width, ld;
+  bool out;
+};
+int check_rows_apart(const char* who, long long rows, std::initializer_list<RowSpan> spans) {
+  for (const RowSpan* a = spans.begin(); a != spans.end(); ++a)
+    for (const RowSpan* b = spans.begin(); b != a; ++b) {
+      if (!a->out && !b->out) continue;
+      const uintptr_t a0 = (uintptr_t)a->p, b0 = (uintptr_t)b->p;
+      if (a0 >= b0 + 2 * ((rows - 1) * b->ld + b->width) || b0 >= a0 + 2 * ((rows - 1) * a->ld + a->width)) continue;
+      if (a->ld == b->ld) {  // columns of one array: b's begin `gap` bytes behind a's in the row
+        const uintptr_t row = 2 * (uintptr_t)a->ld, gap = (b0 % row + row - a0 % row) % row;
+        if (gap >= 2 * (uintptr_t)a->width && row - gap >= 2 * (uintptr_t)b->width) continue;
+      }
+      return fail(MKA_ERR_INVALID_ARG, "%s: %s and %s overlap", who, b->name, a->name);
+    }
+  return MKA_OK;
+}
 
 // Heads, head size and scale shared by the operators' configurations.
 int check_heads(const char* who, int Hq, int Hkv, int dh, float scale, float* out) {
@@ -130,6 +170,9 @@ int check_rows(const char* who, const Kv& kv, int64_t row_stride, int64_t batch_
   if ((int64_t)n * kv.a.Hkv * (kv.a.dh / 16) > 0x7fffff00) return fail(MKA_ERR_UNSUPPORTED, "%s: n too large", who);
   return MKA_OK;
 }
+// Bytes of K's (V's) codes and of its scales.
+size_t code_bytes(const Kv& kv) { return (size_t)kv.a.B * kv.a.Hkv * kv.a.Lmax * kv.a.dh; }
+size_t scale_bytes(const Kv& kv) { return (size_t)kv.a.B * kv.a.Hkv * kv.a.nblk * 4; }
 // Attention limits: grid dimensions and the flat count of 128-position tiles.
 int check_kv8_attention(const char* who, const Kv& kv, int32_t n) {
   if (n < 1) return fail(MKA_ERR_INVALID_ARG, "%s: n must be >= 1", who);
@@ -160,6 +203,10 @@ int mka_kv8_append(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const 
   NEED(k_new); NEED(v_new);
   TRY(check_positions(__func__, pos, "pos", true));
   TRY(check_positions(__func__, count, "count", false));
+  const size_t pb = (size_t)kv.a.B * 4, cb = code_bytes(kv), sb = scale_bytes(kv);
+  TRY(check_apart(__func__, {{"pos", pos, pb, false}, {"count", count, pb, false}, {"cache.k", kv.a.k, cb, true},
+                             {"cache.v", kv.a.v, cb, true}, {"cache.k_scale", kv.a.ks, sb, true},
+                             {"cache.v_scale", kv.a.vs, sb, true}}));
   int* status = device_status();
   if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
   CUDA_TRY(kv8_append(kv.a, k_new, v_new, kv.bf16, row_stride, batch_stride, n, pos, count, status, (cudaStream_t)stream));
@@ -172,10 +219,13 @@ int mka_kv8_read(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const in
   if (!cache) return fail(MKA_ERR_INVALID_ARG, "%s: cache is NULL", __func__);
   TRY(check_kv8(__func__, cfg, cache, &kv));
   TRY(check_rows(__func__, kv, row_stride, batch_stride, n));
-  if (cfg->batch > 1 && batch_stride == 0) return fail(MKA_ERR_INVALID_ARG, "%s: the sequences' outputs are the same rows", __func__);
+  const int64_t width = (int64_t)kv.a.Hkv * kv.a.dh;
+  if (cfg->batch > 1 && batch_stride < width) return fail(MKA_ERR_INVALID_ARG, "%s: the sequences' outputs are the same rows", __func__);
   NEED(k_out); NEED(v_out);
   TRY(check_positions(__func__, first, "first", false));
   TRY(check_positions(__func__, rows, "rows", false));
+  const size_t wb = (size_t)width * (kv.bf16 ? 2 : 4);  // a row: K's and V's rows may lie in each other's gaps
+  TRY(check_apart(__func__, {{"k_out", k_out, wb, true}, {"v_out", v_out, wb, true}}));
   int* status = device_status();
   if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
   CUDA_TRY(kv8_read(kv.a, first, rows, n, k_out, v_out, kv.bf16, row_stride, batch_stride, status, (cudaStream_t)stream));
@@ -201,6 +251,12 @@ int mka_kv8_attention(const mka_kv8_config* cfg, const mka_kv8_cache* cache, con
   size_t stats, scores;
   const size_t need = kv8_attention_scratch(kv.a, kv.G, n, weights != nullptr, &stats, &scores);
   if (ws_bytes < need) return fail(MKA_ERR_WORKSPACE, "%s: ws holds %zu bytes, needs %zu", __func__, ws_bytes, need);
+  const size_t rb = (size_t)kv.a.B * n * kv.Hq * kv.a.dh * (kv.bf16 ? 2 : 4);
+  TRY(check_apart(__func__, {{"lens", lens, (size_t)kv.a.B * 4, false}, {"cache.k", kv.a.k, code_bytes(kv), false},
+                             {"cache.v", kv.a.v, code_bytes(kv), false}, {"cache.k_scale", kv.a.ks, scale_bytes(kv), false},
+                             {"cache.v_scale", kv.a.vs, scale_bytes(kv), false}, {"out", out, rb, true},
+                             {"q", q == out ? nullptr : q, rb, false},  // (in place is safe: a unit's rows are its own)
+                             {"weights", weights, (size_t)kv.a.B * kv.a.Hkv * kv.a.Lmax * 4, true}, {"ws", ws, need, true}}));
   int* status = device_status();
   if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
   Kv8Attn a = {};
@@ -243,6 +299,14 @@ int mka_kv8_evict(const mka_kv8_config* cfg, const mka_kv8_cache* cache, const i
     return fail(MKA_ERR_INVALID_ARG, "%s: weights is NULL or misaligned", __func__);
   NEED(ws);
   if (ws_bytes < mka_kv8_evict_workspace_size(cfg, keep)) return fail(MKA_ERR_WORKSPACE, "%s: ws is too small", __func__);
+  const size_t heads = (size_t)s.a.B * s.a.Hkv, pb = (size_t)s.a.B * 4;
+  TRY(check_apart(__func__, {{"lens", lens, pb, false}, {"weights", weights, heads * s.a.Lmax * 4, false},
+                             {"cache.k", s.a.k, code_bytes(s), false}, {"cache.v", s.a.v, code_bytes(s), false},
+                             {"cache.k_scale", s.a.ks, scale_bytes(s), false}, {"cache.v_scale", s.a.vs, scale_bytes(s), false},
+                             {"dst.k", d.a.k, code_bytes(d), true}, {"dst.v", d.a.v, code_bytes(d), true},
+                             {"dst.k_scale", d.a.ks, scale_bytes(d), true}, {"dst.v_scale", d.a.vs, scale_bytes(d), true},
+                             {"dst_lens", dst_lens, pb, true}, {"dst_weights", dst_weights, heads * d.a.Lmax * 4, true},
+                             {"kept", kept, heads * keep * 4, true}}));
   if (!device_status()) return fail(MKA_ERR_CUDA, "no CUDA device");
   CUDA_TRY(kv8_evict(s.a, lens, weights, keep, first, recent, d.a, dst_lens, dst_weights, kept, (cudaStream_t)stream));
   return MKA_OK;
@@ -255,6 +319,12 @@ int mka_window_attention(const mka_attn_config* cfg, const mka_attn_strides* str
   if (e != MKA_OK) return e;
   NEED(q); NEED(k); NEED(v); NEED(out); OPTIONAL(lse);
   if ((uintptr_t)lens & 3) return fail(MKA_ERR_INVALID_ARG, "%s: lens is not aligned", __func__);
+  const int dq = w.Hq * w.dh, dkv = w.Hkv * w.dh;
+  const long long rows = (long long)w.B * w.S;
+  TRY(check_rows_apart(__func__, rows, {{"q", q, dq, w.ld.q, false}, {"k", k, dkv, w.ld.k, false}, {"v", v, dkv, w.ld.v, false},
+                                        {"out", out, dq, w.ld.o, true}}));
+  TRY(check_apart(__func__, {{"out", out, 2 * ((size_t)(rows - 1) * w.ld.o + dq), true}, {"lens", lens, (size_t)w.B * 4, false},
+                             {"lse", lse, (size_t)w.B * w.Hq * w.Spad * 4, true}}));
   int* status = device_status();
   if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
   AttnArgs a = {};
@@ -287,6 +357,14 @@ int mka_window_attention_backward(const mka_attn_config* cfg, const mka_attn_str
   size_t part = 0;
   const size_t need = window_attention_backward_scratch(w.B, w.S, w.Hq, w.Hkv, w.dh, w.window, w.sinks, &part);
   if (ws_bytes < need) return fail(MKA_ERR_WORKSPACE, "%s: ws holds %zu bytes, needs %zu", __func__, ws_bytes, need);
+  const int nq = w.Hq * w.dh, nkv = w.Hkv * w.dh;
+  const long long rows = (long long)w.B * w.S;
+  TRY(check_rows_apart(__func__, rows, {{"q", q, nq, w.ld.q, false}, {"k", k, nkv, w.ld.k, false}, {"v", v, nkv, w.ld.v, false},
+                                        {"out", out, nq, w.ld.o, false}, {"dout", dout, nq, w.ld.dout, false},
+                                        {"dq", dq, nq, nq, true}, {"dk", dk, nkv, nkv, true}, {"dv", dv, nkv, nkv, true}}));
+  TRY(check_apart(__func__, {{"lens", lens, (size_t)w.B * 4, false}, {"lse", lse, (size_t)w.B * w.Hq * w.Spad * 4, false},
+                             {"dq", dq, 2 * (size_t)rows * nq, true}, {"dk", dk, 2 * (size_t)rows * nkv, true},
+                             {"dv", dv, 2 * (size_t)rows * nkv, true}, {"ws", ws, need, true}}));
   int* status = device_status();
   if (!status) return fail(MKA_ERR_CUDA, "no CUDA device");
   AttnBwdArgs a = {};
