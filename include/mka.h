@@ -285,8 +285,9 @@ MKA_API int mka_window_attention(const mka_attn_config* cfg, const mka_attn_stri
 MKA_API size_t mka_window_attention_backward_workspace_size(const mka_attn_config* cfg);
 /* Gradients of L = sum(dout * out) over the rows in use, from out and lse of mka_window_attention on the
  * same q, k, v, lens: dq [B, S, Hq*dh], dk, dv [B, S, Hkv*dh] bf16, dense (dk and dv summed over the
- * query heads of a KV head in float32, in a fixed order).  ws: 16-byte aligned scratch, used by one call
- * at a time. */
+ * query heads of a KV head in float32, in a fixed order).  Scores, dP, sums and products accumulate in
+ * float32; P and scale * dS (dS) are rounded to bf16 where they enter dV = P^T dO, dQ and dK, and
+ * rowsum(dO o O) takes out as it was rounded.  ws: 16-byte aligned scratch, used by one call at a time. */
 MKA_API int mka_window_attention_backward(const mka_attn_config* cfg, const mka_attn_strides* strides, const void* q,
                                           const void* k, const void* v, const void* out, const float* lse,
                                           const void* dout, const int32_t* lens, void* dq, void* dk, void* dv, void* ws,

@@ -20,6 +20,10 @@
 // each taking 64 of a row's 128 columns; a warp packs its bf16 results into the first 32 columns of
 // its own 64-column range (so neither half overwrites what the other still reads), and the MMAs
 // read K-step kk (16 columns) at packed column kk * 8 + (kk >= 4 ? 32 : 0).
+// Rounding: S, dP, D, P and dS are float32 until P and dS enter their products, in bf16 as the operands that they
+// meet there (2^-8 of themselves each; hi and lo parts would add three products to the five).  D = rowsum(dO * O)
+// takes the rounded O that the caller kept.  Against 64 bits the gradients' relative error is 0.0025 where one
+// rounding of exact results leaves 0.0017.
 //
 // WN (window with sinks, see AttnArgs): position t sees j <= t with j > t - window or j < sinks, over
 // lens[b] rows; gradients leave as bf16.  dQ streams the sink tiles before the window and the window's
