@@ -43,7 +43,7 @@ def decode(q, k, v, vs, p, window, sinks, scale, bf16):
     Scores are float32 sums of dh exact products (ds); 2^x is good to 2^-22 and its argument, below 2^7, to
     2^-17; a lane adds up a few hundred positions at most: 2^-15 covers both.  P is rounded to half, 2^-11 of
     itself or 2^-34 of the largest weight times V scale (float32 rows: 2^-22, 2^-45); the output once to its type."""
-    j = torch.arange(k.shape[0])
+    j = torch.arange(k.shape[0], device=k.device)
     m = j <= p
     if window:
         m = m & ((j > p - window) | (j < sinks))
@@ -56,7 +56,7 @@ def decode(q, k, v, vs, p, window, sinks, scale, bf16):
     e = (2 * ds + (2.0 ** -11 if bf16 else 2.0 ** -22)) * (w @ v.abs())
     e = e + (2.0 ** -34 if bf16 else 2.0 ** -45) * top * (v / vs[:, None]).abs().sum(0)
     e = e + (ref.BF16 if bf16 else 2.0 ** -23) * (o.abs() + e)
-    full, bound = torch.zeros(q.shape[0], len(j), dtype=torch.float64), torch.zeros(q.shape[0], len(j), dtype=torch.float64)
+    full, bound = (torch.zeros(q.shape[0], len(j), dtype=torch.float64, device=k.device) for _ in range(2))
     full[:, m], bound[:, m] = w, 2 * ds * w
     return o, full, e, bound
 
